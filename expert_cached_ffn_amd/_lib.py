@@ -12,7 +12,7 @@ LIB_PATH = os.environ.get("FTMOE_LIB") or os.path.join(PKG, "libftmoe.so")
 FT_OK, FT_EINVAL, FT_ENOTSUP, FT_ECAPACITY, FT_EHIP = 0, -1, -2, -3, -4
 STATUS_NAMES = {0: "FT_OK", -1: "FT_EINVAL", -2: "FT_ENOTSUP", -3: "FT_ECAPACITY", -4: "FT_EHIP"}
 # dtypes / gating / workspace selectors
-FT_F32, FT_BF16, FT_MXFP4, FT_NVFP4 = 0, 1, 2, 3
+FT_F32, FT_BF16, FT_MXFP4, FT_NVFP4, FT_FP8 = 0, 1, 2, 3, 4
 FT_SOFTMAX, FT_SIGMOID = 0, 1
 FT_WS_PERMUTE, FT_WS_FFN, FT_WS_ROUTE_PERMUTE, FT_WS_LAYER = 1, 2, 3, 4
 FT_FFN_EXACT, FT_FFN_NATIVE_MX = 0, 1
@@ -30,6 +30,7 @@ EXPORTS = [
     "ft_expert_cache_stage_cpu_misses", "ft_expert_cache_run_cpu_misses", "ft_expert_cache_step_split",
     "ft_expert_cache_wait_fills", "ft_expert_cache_plan", "ft_expert_cache_fill", "ft_expert_cache_set_trace",
     "ft_moe_grouped_ffn_noalloc", "ft_noalloc_scratch_bytes", "ft_moe_layer", "ft_read_checksum",
+    "ft_fp8_quantize", "ft_fp8_gemm", "ft_grouped_gemm",
 ]
 
 
@@ -68,7 +69,7 @@ def lib() -> C.CDLL:
     if not os.path.exists(LIB_PATH):
         raise LibraryMissing(f"{LIB_PATH} not found: build it with `python -m expert_cached_ffn_amd.build`")
     L = C.CDLL(LIB_PATH)
-    p, i32, sz, u64 = C.c_void_p, C.c_int32, C.c_size_t, C.c_uint64
+    p, i32, sz, u64, i64 = C.c_void_p, C.c_int32, C.c_size_t, C.c_uint64, C.c_int64
     L.ft_last_error.restype = C.c_char_p
     L.ft_last_error.argtypes = []
     L.ft_version.restype = C.c_char_p
@@ -124,6 +125,12 @@ def lib() -> C.CDLL:
     L.ft_moe_route_permute.argtypes = [p, i32, p, p, i32, i32, i32, i32, i32, i32, p, p, p, p, p, p, sz, p]
     L.ft_mxfp8_quantize.restype = i32
     L.ft_mxfp8_quantize.argtypes = [p, C.c_int64, i32, i32, p, p, p]
+    L.ft_fp8_quantize.restype = i32
+    L.ft_fp8_quantize.argtypes = [p, i32, i64, i64, i32, i32, p, i64, p, p]
+    L.ft_fp8_gemm.restype = i32
+    L.ft_fp8_gemm.argtypes = [p, i64, p, p, i64, p, i64, i32, i32, i32, p, i64, p]
+    L.ft_grouped_gemm.restype = i32
+    L.ft_grouped_gemm.argtypes = [i32, p, i64, p, p, u64, u64, u64, i32, p, i32, i32, i32, p, p, i32, i32, i32, p, i64, p]
     L.ft_moe_combine.restype = i32
     L.ft_moe_combine.argtypes = [p, p, p, p, i32, i32, i32, i32, p, p]
     L.ft_expert_cache_create.restype = i32
@@ -140,6 +147,5 @@ def lib() -> C.CDLL:
     L.ft_expert_cache_destroy.argtypes = [p]
     L.ft_workspace_bytes.restype = sz
     L.ft_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
-    _ = u64
     _lib = L
     return L

@@ -67,6 +67,17 @@ extern "C" ft_status ft_expert_layout_init(int32_t wdtype, int32_t H, int32_t I,
       L.off_sdown = place(n / 16);
       L.off_tscale = place(3 * 4);
       break;
+    case FT_FP8: {
+      FT_REQUIRE(H % 16 == 0 && I % 16 == 0, "ft_expert_layout_init: FP8 needs H and I multiples of 16");
+      const uint64_t ns = ((uint64_t(H) + 127) / 128) * ((uint64_t(I) + 127) / 128);
+      L.off_gate = place(n);
+      L.off_up = place(n);
+      L.off_down = place(n);
+      L.off_sgate = place(ns * 4);
+      L.off_sup = place(ns * 4);
+      L.off_sdown = place(ns * 4);
+      break;
+    }
     default:
       return ft::fail(FT_EINVAL, "ft_expert_layout_init: unknown weight dtype");
   }

@@ -24,6 +24,7 @@
 #include "gemv_token.hpp"
 #include "gemm_prefill.hpp"
 #include "gemm_mx.hpp"
+#include "group_ffn.hpp"
 
 namespace ft {
 
@@ -52,8 +53,8 @@ size_t ffn_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I
   (void)E;
   const uint64_t rows = uint64_t(T) * uint64_t(k) + uint64_t(T);
   const uint64_t b = (rows * uint64_t(I) * 4 + 255) / 256 * 256;  // fp32 hidden rows (bf16 paths use half)
-  const uint64_t mx = mx_workspace_layout(T, k, H, I).total;
-  return size_t(b > mx ? b : mx);
+  const uint64_t mx = mx_workspace_layout(T, k, H, I).total, fp8 = fp8_ffn_workspace_bytes(T, k, H, I);
+  return size_t(std::max(b, std::max(mx, fp8)));
 }
 
 // Block-wide: index of the aidx-th expert with a non-empty segment (ascending
@@ -764,6 +765,9 @@ static ft_status ffn_check(const ft_expert_layout *L, const void *slot_pool, int
   } else if (wd == FT_NVFP4) {
     FT_REQUIRE(x_dtype == FT_BF16, "ft_moe_grouped_ffn: NVFP4 weights need bf16 activations");
     FT_SUPPORTED(H % 128 == 0 && I % 128 == 0, "ft_moe_grouped_ffn: NVFP4 weights need H, I multiples of 128");
+  } else if (wd == FT_FP8) {
+    FT_REQUIRE(x_dtype == FT_BF16, "ft_moe_grouped_ffn: FP8 weights need bf16 activations");
+    FT_SUPPORTED(H % 16 == 0 && I % 16 == 0, "ft_moe_grouped_ffn: FP8 weights need H, I multiples of 16");
   } else {
     return fail(FT_EINVAL, "ft_moe_grouped_ffn: unknown weight dtype in layout");
   }
@@ -857,6 +861,15 @@ extern "C" ft_status ft_moe_grouped_ffn(const ft_expert_layout *L, const void *s
         return st;
       if ((st = launch_mx_gemm<false>(m2, stream, "ffn_mx_gemm_kernel<down>")) != FT_OK) return st;
     }
+    clear_error();
+    return FT_OK;
+  }
+
+  if (wd == FT_FP8) {
+    const ft_status st = fp8_ffn(Fp8Ffn{L, slot_pool, n_slots, slot_of_expert, shared_blob, x, T, k, E, expert_offsets,
+                                        sorted_rows, y_rows, y_shared, run1, run2, workspace},
+                                 stream);
+    if (st != FT_OK) return st;
     clear_error();
     return FT_OK;
   }

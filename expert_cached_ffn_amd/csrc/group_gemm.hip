@@ -1,0 +1,245 @@
+// ft_fp8_gemm, ft_grouped_gemm and the FP8 experts of ft_moe_grouped_ffn: the
+// entry points and launches of the products in group_gemm.hpp.
+#include "ft_internal.hpp"
+#include "group_gemm.hpp"
+#include "group_ffn.hpp"
+
+namespace ft {
+
+template <int TY, int EP, int WM, int WN, int MT, int NT, int STAGES>
+__global__ __launch_bounds__(WM * WN * 64) void group_gemm_kernel(GroupArgs a) {
+  using G = GroupTile<TY, EP, WM, WN, MT, NT, STAGES>;
+  // one array per step, so that reads of one do not wait for loads into another
+  __shared__ __attribute__((aligned(16))) uint8_t l0[G::STAGE_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t l1[G::STAGE_BYTES];
+  if constexpr (STAGES == 2) {
+    G::run(a, typename G::Ring{{l0, l1}});
+  } else {
+    static_assert(STAGES == 3, "two or three steps");
+    __shared__ __attribute__((aligned(16))) uint8_t l2[G::STAGE_BYTES];
+    G::run(a, typename G::Ring{{l0, l1, l2}});
+  }
+}
+
+// Most row tiles that the groups can have.
+static int row_tiles(const GroupArgs &a, int BM) {
+  if (a.offsets == nullptr) return cdiv(a.rows, BM);
+  return a.rows / BM + std::min(a.E, a.rows) + (a.shared_blob != nullptr ? cdiv(a.T, BM) : 0);
+}
+
+template <int TY, int EP, int WM, int WN, int MT, int NT, int STAGES>
+static ft_status launch_tiles(GroupArgs a, hipStream_t stream) {
+  using G = GroupTile<TY, EP, WM, WN, MT, NT, STAGES>;
+  a.n_ntiles = cdiv(a.N, G::NCOL);
+  const int64_t items = int64_t(row_tiles(a, G::BM)) * a.n_ntiles;
+  FT_SUPPORTED(items < (int64_t(1) << 31) - 8, "grouped product: more than 2^31 tiles");
+  const unsigned grid = unsigned(cdiv<int64_t>(items, 8) * 8);
+  hipLaunchKernelGGL((group_gemm_kernel<TY, EP, WM, WN, MT, NT, STAGES>), dim3(grid), dim3(G::THREADS), 0, stream, a);
+  FT_LAUNCHED("group_gemm_kernel");
+  return FT_OK;
+}
+
+template <int TY>
+static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
+  return launch_tiles<TY, GE_OUT, 2, 2, 2, 2, 3>(a, stream);
+}
+
+static ft_status group_products(int dtype, const GroupArgs &a, hipStream_t stream) {
+  if (a.rows == 0 || a.N == 0) return FT_OK;
+  if (dtype == FT_BF16) return launch_products<GT_BF16>(a, stream);
+  return a.out_bf16 ? launch_products<GT_FP8>(a, stream) : launch_products<GT_FP8X>(a, stream);
+}
+
+// ------------------------------------------------------------------ FP8 experts
+
+// Workspace: the tokens' codes and scales, the hidden rows in fp32, their codes and scales.
+struct Fp8FfnWorkspace {
+  uint64_t xq, xs, h, hq, hs, total;
+};
+static Fp8FfnWorkspace fp8_ffn_workspace(int64_t T, int64_t k, int64_t H, int64_t I) {
+  auto al = [](uint64_t b) { return (b + 255) / 256 * 256; };
+  const uint64_t rows = uint64_t(T * k + T);
+  Fp8FfnWorkspace w;
+  w.h = 0;
+  w.hq = w.h + al(rows * I * 4);
+  w.hs = w.hq + al(rows * I);
+  w.xq = w.hs + al(rows * cdiv<int64_t>(I, kFp8Block) * 4);
+  w.xs = w.xq + al(uint64_t(T * H));
+  w.total = w.xs + al(uint64_t(T) * cdiv<int64_t>(H, kFp8Block) * 4);
+  return w;
+}
+
+size_t fp8_ffn_workspace_bytes(int32_t T, int32_t k, int32_t H, int32_t I) {
+  return size_t(fp8_ffn_workspace(T, k, H, I).total);
+}
+
+ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
+  const ft_expert_layout &L = *f.L;
+  const int H = L.H, I = L.I, routed = f.T * f.k, rows = routed + (f.shared_blob != nullptr ? f.T : 0);
+  const Fp8FfnWorkspace W = fp8_ffn_workspace(f.T, f.k, H, I);
+  uint8_t *ws = static_cast<uint8_t *>(f.workspace);
+  GroupArgs a{};
+  a.pool = static_cast<const uint8_t *>(f.slot_pool);
+  a.expert_bytes = L.expert_bytes;
+  a.slots = f.slot_of_expert;
+  a.n_slots = f.n_slots;
+  a.shared_blob = static_cast<const uint8_t *>(f.shared_blob);
+  a.offsets = f.expert_offsets;
+  a.E = f.E;
+  a.rows = routed;
+  a.T = f.T;
+  a.k = f.k;
+  ft_status st;
+  if (f.gate_up) {
+    st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, reinterpret_cast<float *>(ws + W.xs), stream);
+    if (st != FT_OK) return st;
+    GroupArgs g = a;
+    g.A = ws + W.xq;
+    g.lda = H;
+    g.As = reinterpret_cast<const float *>(ws + W.xs);
+    g.off_w0 = L.off_gate;
+    g.off_w1 = L.off_up;
+    g.off_s0 = L.off_sgate;
+    g.off_s1 = L.off_sup;
+    g.ldw = g.Kb = H;
+    g.KB = cdiv(H, kFp8Block);
+    g.N = I;
+    g.sorted_rows = f.sorted_rows;
+    g.a_rows = f.T;
+    g.out = ws + W.h;
+    g.ldo = I;
+    if ((st = launch_tiles<GT_FP8, GE_GLU, 2, 2, 2, 4, 3>(g, stream)) != FT_OK) return st;
+  }
+  if (f.down) {
+    st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, reinterpret_cast<float *>(ws + W.hs), stream);
+    if (st != FT_OK) return st;
+    GroupArgs d = a;
+    d.A = ws + W.hq;
+    d.lda = I;
+    d.As = reinterpret_cast<const float *>(ws + W.hs);
+    d.off_w0 = d.off_w1 = L.off_down;
+    d.off_s0 = d.off_s1 = L.off_sdown;
+    d.ldw = d.Kb = I;
+    d.KB = cdiv(I, kFp8Block);
+    d.N = H;
+    d.a_rows = rows;
+    d.a_shared0 = routed;
+    d.out = f.y_rows;
+    d.ldo = H;
+    d.out_shared = f.y_shared;
+    if ((st = launch_tiles<GT_FP8, GE_OUT, 2, 2, 2, 2, 3>(d, stream)) != FT_OK) return st;
+  }
+  return FT_OK;
+}
+
+}  // namespace ft
+
+using namespace ft;
+
+constexpr int64_t kMaxPitch = int64_t(1) << 22;  // bytes of a row: a tile's rows stay under 2 GiB
+
+extern "C" ft_status ft_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, const uint8_t *w, int64_t ldw,
+                                 const float *w_scales, int64_t M, int32_t N, int32_t K, int32_t out_dtype, void *out,
+                                 int64_t ldo, hipStream_t stream) {
+  FT_REQUIRE(M >= 0 && N >= 0 && K >= 1, "ft_fp8_gemm: need M >= 0, N >= 0, K >= 1");
+  FT_REQUIRE(out_dtype == FT_BF16 || out_dtype == FT_F32, "ft_fp8_gemm: out_dtype must be FT_BF16 or FT_F32");
+  FT_SUPPORTED(K % 16 == 0, "ft_fp8_gemm: K must be a multiple of 16");
+  FT_REQUIRE(lda >= K && ldw >= K && ldo >= N, "ft_fp8_gemm: row pitch below the row's length");
+  FT_SUPPORTED(M < (int64_t(1) << 31) - 512 && lda <= kMaxPitch && ldw <= kMaxPitch,
+               "ft_fp8_gemm: M above 2^31 - 512 or a row pitch above 4 MiB");
+  if (M == 0 || N == 0) {
+    clear_error();
+    return FT_OK;
+  }
+  FT_REQUIRE(a && a_scales && w && w_scales && out, "ft_fp8_gemm: NULL pointer argument");
+  FT_REQUIRE(lda % 16 == 0 && ldw % 16 == 0 && aligned(a, 16) && aligned(w, 16) && aligned(out, 16) &&
+                 aligned(a_scales, 4) && aligned(w_scales, 4),
+             "ft_fp8_gemm: a, w and out must be 16-byte aligned, lda and ldw multiples of 16");
+  GroupArgs g{};
+  g.A = a;
+  g.lda = lda;
+  g.As = a_scales;
+  g.pool = w;
+  g.n_slots = 1;
+  g.off_s0 = uint64_t(reinterpret_cast<uintptr_t>(w_scales) - reinterpret_cast<uintptr_t>(w));
+  g.ldw = ldw;
+  g.Kb = K;
+  g.KB = cdiv(K, kFp8Block);
+  g.N = N;
+  g.E = 1;
+  g.rows = int(M);
+  g.T = int(M);
+  g.k = 1;
+  g.a_rows = M;
+  g.out = out;
+  g.out_bf16 = out_dtype == FT_BF16;
+  g.ldo = ldo;
+  const ft_status st = group_products(FT_FP8, g, stream);
+  if (st != FT_OK) return st;
+  clear_error();
+  return FT_OK;
+}
+
+extern "C" ft_status ft_grouped_gemm(int32_t dtype, const void *a, int64_t lda, const float *a_scales,
+                                     const void *slot_pool, uint64_t expert_bytes, uint64_t off_w, uint64_t off_s,
+                                     int32_t n_slots, const int32_t *slot_of_expert, int32_t T, int32_t k, int32_t E,
+                                     const int32_t *expert_offsets, const int32_t *sorted_rows, int32_t N, int32_t K,
+                                     int32_t out_dtype, void *out, int64_t ldo, hipStream_t stream) {
+  FT_REQUIRE(dtype == FT_BF16 || dtype == FT_FP8, "ft_grouped_gemm: dtype must be FT_BF16 or FT_FP8");
+  FT_REQUIRE(out_dtype == FT_BF16 || out_dtype == FT_F32, "ft_grouped_gemm: out_dtype must be FT_BF16 or FT_F32");
+  FT_REQUIRE(T >= 0 && k >= 1 && E >= 1 && N >= 0 && K >= 1,
+             "ft_grouped_gemm: need T >= 0, k >= 1, E >= 1, N >= 0, K >= 1");
+  FT_SUPPORTED(E <= 4096, "ft_grouped_gemm: E > 4096");
+  FT_REQUIRE(int64_t(T) * k < (int64_t(1) << 31) - 512, "ft_grouped_gemm: T*k too large");
+  const int es = dtype == FT_BF16 ? 2 : 1;
+  FT_SUPPORTED(K % (16 / es) == 0, "ft_grouped_gemm: K must be a multiple of 16 (bf16: of 8)");
+  FT_REQUIRE(lda >= K && ldo >= N, "ft_grouped_gemm: row pitch below the row's length");
+  FT_SUPPORTED(lda * es <= kMaxPitch && int64_t(K) * es <= kMaxPitch, "ft_grouped_gemm: a row pitch above 4 MiB");
+  FT_SUPPORTED(sorted_rows == nullptr || int64_t(T) * lda * es < (int64_t(1) << 31),
+               "ft_grouped_gemm: gathered rows of 2 GiB or more");
+  if (T == 0 || N == 0) {
+    clear_error();
+    return FT_OK;
+  }
+  FT_REQUIRE(a && slot_pool && expert_offsets && out && (dtype == FT_BF16 || a_scales),
+             "ft_grouped_gemm: NULL pointer argument");
+  FT_REQUIRE(n_slots >= 1 && (slot_of_expert != nullptr || n_slots >= E),
+             "ft_grouped_gemm: n_slots must be >= 1, and >= E when slot_of_expert is NULL");
+  FT_REQUIRE(aligned(a, 16) && lda * es % 16 == 0 && aligned(out, 16) && aligned(a_scales, 4),
+             "ft_grouped_gemm: a and out must be 16-byte aligned, rows of a a multiple of 16 bytes apart");
+  FT_REQUIRE(aligned(slot_pool, 16) && expert_bytes % 16 == 0 && off_w % 16 == 0 && off_s % 4 == 0,
+             "ft_grouped_gemm: weights must be 16-byte aligned (scales 4-byte)");
+  const int KB = cdiv(K, kFp8Block);
+  const uint64_t wb = uint64_t(N) * K * es, sb = dtype == FT_FP8 ? uint64_t(cdiv(N, kFp8Block)) * KB * 4 : 0;
+  FT_REQUIRE(off_w <= expert_bytes && wb <= expert_bytes - off_w &&
+                 (sb == 0 || (off_s <= expert_bytes && sb <= expert_bytes - off_s)),
+             "ft_grouped_gemm: weights or scales reach past expert_bytes");
+  GroupArgs g{};
+  g.A = static_cast<const uint8_t *>(a);
+  g.lda = lda * es;
+  g.As = a_scales;
+  g.pool = static_cast<const uint8_t *>(slot_pool);
+  g.expert_bytes = expert_bytes;
+  g.slots = slot_of_expert;
+  g.n_slots = n_slots;
+  g.off_w0 = off_w;
+  g.off_s0 = off_s;
+  g.ldw = int64_t(K) * es;
+  g.Kb = K * es;
+  g.KB = KB;
+  g.N = N;
+  g.offsets = expert_offsets;
+  g.E = E;
+  g.rows = T * k;
+  g.T = T;
+  g.k = k;
+  g.sorted_rows = sorted_rows;
+  g.a_rows = sorted_rows != nullptr ? T : int64_t(T) * k;
+  g.out = out;
+  g.out_bf16 = out_dtype == FT_BF16;
+  g.ldo = ldo;
+  const ft_status st = group_products(dtype, g, stream);
+  if (st != FT_OK) return st;
+  clear_error();
+  return FT_OK;
+}

@@ -153,6 +153,26 @@ def ft_mxfp8_quantize(x, ldx: int, n: int, K: int, codes, scales, stream=None) -
     _check(_lib.lib().ft_mxfp8_quantize(_ptr(x), ldx, n, K, _ptr(codes), _ptr(scales), _stream(stream)))
 
 
+def ft_fp8_quantize(x, x_dtype: int, ldx: int, n: int, K: int, block_rows: int, codes, ldc: int, scales,
+                    stream=None) -> None:
+    _check(_lib.lib().ft_fp8_quantize(_ptr(x), x_dtype, ldx, n, K, block_rows, _ptr(codes), ldc, _ptr(scales),
+                                      _stream(stream)))
+
+
+def ft_fp8_gemm(a, lda: int, a_scales, w, ldw: int, w_scales, M: int, N: int, K: int, out_dtype: int, out, ldo: int,
+                stream=None) -> None:
+    _check(_lib.lib().ft_fp8_gemm(_ptr(a), lda, _ptr(a_scales), _ptr(w), ldw, _ptr(w_scales), M, N, K, out_dtype,
+                                  _ptr(out), ldo, _stream(stream)))
+
+
+def ft_grouped_gemm(dtype: int, a, lda: int, a_scales, slot_pool, expert_bytes: int, off_w: int, off_s: int,
+                    n_slots: int, slot_of_expert, T: int, k: int, E: int, expert_offsets, sorted_rows, N: int, K: int,
+                    out_dtype: int, out, ldo: int, stream=None) -> None:
+    _check(_lib.lib().ft_grouped_gemm(dtype, _ptr(a), lda, _ptr(a_scales), _ptr(slot_pool), expert_bytes, off_w, off_s,
+                                      n_slots, _ptr(slot_of_expert), T, k, E, _ptr(expert_offsets), _ptr(sorted_rows),
+                                      N, K, out_dtype, _ptr(out), ldo, _stream(stream)))
+
+
 def ft_moe_combine(y_rows, topk_w, row_pos, y_shared, T: int, k: int, H: int, out_dtype: int, out,
                    stream=None) -> None:
     _check(_lib.lib().ft_moe_combine(_ptr(y_rows), _ptr(topk_w), _ptr(row_pos), _ptr(y_shared), T, k, H,

@@ -67,7 +67,7 @@ const char *ft_last_error(void);
 /* Library version string, e.g. "ftmoe 0.1 gfx950". */
 const char *ft_version(void);
 
-typedef enum { FT_F32 = 0, FT_BF16 = 1, FT_MXFP4 = 2, FT_NVFP4 = 3 } ft_dtype;
+typedef enum { FT_F32 = 0, FT_BF16 = 1, FT_MXFP4 = 2, FT_NVFP4 = 3, FT_FP8 = 4 } ft_dtype;
 typedef enum { FT_SOFTMAX = 0, FT_SIGMOID = 1 } ft_gating;
 
 /* slot_of_expert value for an expert whose rows a grouped-FFN call must leave
@@ -84,7 +84,7 @@ typedef enum { FT_SOFTMAX = 0, FT_SIGMOID = 1 } ft_gating;
  * 4090 page, "Cómo funciona la jerarquía de memoria MoE": an entry is a whole
  * expert under one logical mapping on CPU and GPU).
  *
- * Blob = [gate][up][down] (+ for MXFP4: [gate scales][up scales][down scales]),
+ * Blob = [gate][up][down] (+ for MXFP4, NVFP4 and FP8: [gate scales][up scales][down scales]),
  * each part starting at a 256-byte boundary, expert_bytes rounded up to 4 KiB.
  *   gate, up : [I, H]   (contraction axis H contiguous)
  *   down     : [H, I]   (contraction axis I contiguous)
@@ -98,6 +98,9 @@ typedef enum { FT_SOFTMAX = 0, FT_SIGMOID = 1 } ft_gating;
  *   [rows, K/16] bytes, FP8 E4M3 (OCP), one per 16 consecutive elements; and
  *   three fp32 tensor scales (gate, up, down) at off_tscale.  Element =
  *   E2M1 x E4M3(block scale) x tensor scale.
+ * FT_FP8 (the form of block-scaled FP8 checkpoints; not on the pages): FP8 E4M3
+ *   (OCP) codes [rows, K] bytes; scales [ceil(rows / 128), ceil(K / 128)] fp32,
+ *   one per 128 x 128 block of the matrix.  Element = E4M3 x scale.
  */
 typedef struct {
   int32_t wdtype;        /* ft_dtype of the expert weights                     */
@@ -105,13 +108,13 @@ typedef struct {
   int32_t reserved;
   uint64_t expert_bytes; /* bytes of one blob (a multiple of 4096)             */
   uint64_t off_gate, off_up, off_down;      /* byte offsets of the three parts */
-  uint64_t off_sgate, off_sup, off_sdown;   /* MXFP4 / NVFP4 scale parts (0 otherwise) */
+  uint64_t off_sgate, off_sup, off_sdown;   /* MXFP4 / NVFP4 / FP8 scale parts (0 otherwise) */
   uint64_t off_tscale;   /* NVFP4: 3 fp32 tensor scales (gate, up, down); 0 otherwise */
 } ft_expert_layout;
 
 /* Fill *out for experts of type wdtype.  Host only, pure.
  * Errors: FT_EINVAL (out NULL, H or I < 1, unknown dtype, MXFP4 with H or I
- * not a multiple of 32, NVFP4 with H or I not a multiple of 16). */
+ * not a multiple of 32, NVFP4 or FP8 with H or I not a multiple of 16). */
 ft_status ft_expert_layout_init(int32_t wdtype, int32_t H, int32_t I, ft_expert_layout *out);
 
 /* ------------------------------------------------------------------------ */
@@ -190,7 +193,7 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  * non-empty segment with another negative slot, or a slot >= n_slots, is a
  * caller error: nothing is read for it and its y rows are written as NaN.
  * x [T, H] of x_dtype (FT_F32 with FT_F32 weights, FT_BF16 with FT_BF16 or
- *   FT_MXFP4 weights).
+ *   FT_MXFP4, FT_NVFP4 or FT_FP8 weights).
  * y_rows [T*k, H] fp32, permuted order (row i belongs to sorted_rows[i]).
  * shared_blob (nullable): one more expert in the same layout, applied to every
  *   token with weight 1, written to y_shared [T, H] fp32 (required iff
@@ -207,6 +210,10 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  *     quantization (a few percent); they match a float64 evaluation of the
  *     same quantized operands.
  *   Other values: FT_ENOTSUP.
+ *   FT_FP8 weights take FT_FFN_EXACT, in which the activations join them in
+ *   FP8: x and the fp32 hidden vector are quantized exactly as ft_fp8_quantize
+ *   does with block_rows 1, and the products are those of ft_fp8_gemm with
+ *   bf16 outputs (sums good to about 16 bits), y_rows being fp32.
  * mode, stage bits: FT_FFN_GATE_UP_ONLY runs only the gate/up + SwiGLU stage
  *   (y is not written); FT_FFN_DOWN_ONLY runs only the down projection from
  *   the hidden rows in `workspace` (left there by a FT_FFN_GATE_UP_ONLY call
@@ -217,7 +224,7 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  *   weights keep fp32 rows there.
  * workspace: ft_workspace_bytes(FT_WS_FFN, T, k, E, H, I) bytes.
  * Limits: FT_BF16 weights need H, I multiples of 128; FT_MXFP4 multiples of
- *   256; E <= 4096.  MXFP4 scale bytes must lie in 2..252 (every decoded value
+ *   256; FT_FP8 multiples of 16; E <= 4096.  MXFP4 scale bytes must lie in 2..252 (every decoded value
  *   is then an exact bf16).  Buffers 16-byte aligned, slot_pool and blobs
  *   256-byte aligned.
  */
@@ -346,6 +353,88 @@ ft_status ft_cpu_miss_rows(const ft_expert_layout *L, const void *bank, int32_t 
  */
 ft_status ft_mxfp8_quantize(const void *x, int64_t ldx, int32_t n, int32_t K, uint8_t *codes,
                             uint8_t *scales, hipStream_t stream);
+
+/*
+ * ft_fp8_quantize -- rows to FP8 with one scale per block of 128: the operand
+ * format of the two products below and of FT_FP8 experts (the pages name
+ * quantized experts of other formats only; the format is that of block-scaled
+ * FP8 checkpoints).  x [n, K] of x_dtype (FT_BF16 or FT_F32), row pitch ldx
+ * elements; blocks of block_rows x 128 elements, block_rows 1 (activations) or
+ * 128 (weights), the last ones partial where n or K is no multiple.
+ *   scale = 2^max(-126, ceil(log2(amax / 448))), amax the block's largest
+ *           magnitude: the smallest power of two that brings it within E4M3
+ *   code  = the FP8 E4M3 code nearest x / scale (exact quotient), ties to even
+ * codes [n, K] bytes, row pitch ldc; scales [ceil(n / block_rows),
+ * ceil(K / 128)] fp32, row-major.  A block that holds a NaN or an infinity gets
+ * scale NaN and codes 0, so every product over it is NaN; other blocks are not
+ * touched by it.  Bytes of codes behind column K of a row are left as they were.
+ * n = 0 or K = 0 is a no-op.  Errors: K not a multiple of 16, n >= 2^31 or more
+ * than 2^34 blocks -> FT_ENOTSUP; x, codes not 16-byte aligned, ldx not a
+ * multiple of 8, ldc of 16, a pitch below K, block_rows other than 1 and 128,
+ * NULL pointers -> FT_EINVAL.
+ */
+ft_status ft_fp8_quantize(const void *x, int32_t x_dtype, int64_t ldx, int64_t n, int32_t K,
+                          int32_t block_rows, uint8_t *codes, int64_t ldc, float *scales,
+                          hipStream_t stream);
+
+/*
+ * ft_fp8_gemm -- the product of two block-scaled FP8 matrices (a dense layer of
+ * an FP8 model, e.g. a shared expert's projection outside the expert cache):
+ *   out[m, n] = sum_b a_scales[m, b] * w_scales[n / 128, b]
+ *                     * sum_{k in block b} a[m, k] * w[n, k],   b = k / 128
+ * a [M, K] E4M3 codes, row pitch lda bytes, a_scales [M, ceil(K / 128)];
+ * w [N, K] E4M3 codes, row pitch ldw bytes, w_scales [ceil(N / 128),
+ * ceil(K / 128)]; any fp32 scales; out [M, N] of out_dtype (FT_BF16, rounded
+ * once to nearest even, or FT_F32), row pitch ldo elements.  Columns of out
+ * behind N are left as they were; out must not overlap the operands.
+ * Sums: FT_F32 outputs are summed in fp32 throughout.  FT_BF16 outputs of more
+ * than a few rows take the FP8 matrix instruction, whose sum over one block of
+ * 128 keeps about 16 bits (relative error 1.5e-5 for bell-shaped codes, at most
+ * 2e-4 of the block's sum of magnitudes), the blocks being added in fp32.
+ * Codes 0x7f / 0xff are NaN.  M = 0 or N = 0 is a no-op.
+ * Limits (FT_ENOTSUP): K a multiple of 16, pitches of a and w at most 4 MiB,
+ * M < 2^31 - 512.  FT_EINVAL: a, w or out not 16-byte aligned, lda or ldw not
+ * a multiple of 16 or below K, ldo below N, K < 1, NULL pointers.
+ */
+ft_status ft_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, const uint8_t *w, int64_t ldw,
+                      const float *w_scales, int64_t M, int32_t N, int32_t K, int32_t out_dtype,
+                      void *out, int64_t ldo, hipStream_t stream);
+
+/*
+ * ft_grouped_gemm -- one matrix product per expert over ragged groups of rows:
+ * the product inside ft_moe_grouped_ffn on its own, for experts of another form
+ * than SwiGLU, for a single projection of an expert blob, and for any rows
+ * grouped by weights (the pages route each token to a few experts and read
+ * their weights from cache slots: FreeToken quantization page, "Cómo se
+ * desplazan los pesos MoE cuantizados por la memoria").
+ *   out[p] = A[src(p)] * W_e^T   for expert_offsets[e] <= p < expert_offsets[e+1]
+ * src(p) = sorted_rows[p] / k (a [T, K], one row per token) or, with
+ * sorted_rows NULL, p (a [T*k, K], rows already in permuted order; k = 1 and T
+ * rows for groups that no routing made).  Expert e's weights are [N, K] with
+ * rows contiguous at slot_pool + slot_of_expert[e] * expert_bytes + off_w
+ * (slot_of_expert NULL: slot e; n_slots slots in the pool, >= E then).
+ * dtype FT_BF16: a and weights bf16, a_scales and off_s unused.
+ * dtype FT_FP8: E4M3 codes with a_scales [rows of a, ceil(K / 128)] and weight
+ *   scales [ceil(N / 128), ceil(K / 128)] fp32 at byte off_s of the slot, as in
+ *   ft_fp8_gemm, whose remark on sums holds here too.  (FP8 blobs:
+ *   off_w = off_gate and off_s = off_sgate of the layout, and so on.)
+ * lda in elements of a.  out [T*k, N] of out_dtype (FT_BF16 or FT_F32), row
+ * pitch ldo elements; rows from expert_offsets[E] on and columns behind N are
+ * left as they were.  Offsets are held inside [0, T*k].  A group whose slot is
+ * FT_SLOT_SKIP is left untouched; with another negative slot or one >= n_slots
+ * its rows are written as NaN; a row whose sorted_rows entry names no token is
+ * computed from zeros.  T = 0 or N = 0 is a no-op.
+ * Limits (FT_ENOTSUP): E <= 4096, K a multiple of 16 (FT_BF16: of 8), pitches
+ * at most 4 MiB, gathered rows (T * lda) under 2 GiB.  FT_EINVAL: other dtypes,
+ * a, out, slot_pool, expert_bytes, off_w not 16-byte aligned (off_s 4), lda
+ * below K or not a multiple of 16 bytes, ldo below N, T*k >= 2^31 - 512,
+ * weights or scales reaching past expert_bytes, NULL pointers.
+ */
+ft_status ft_grouped_gemm(int32_t dtype, const void *a, int64_t lda, const float *a_scales,
+                          const void *slot_pool, uint64_t expert_bytes, uint64_t off_w, uint64_t off_s,
+                          int32_t n_slots, const int32_t *slot_of_expert, int32_t T, int32_t k, int32_t E,
+                          const int32_t *expert_offsets, const int32_t *sorted_rows, int32_t N, int32_t K,
+                          int32_t out_dtype, void *out, int64_t ldo, hipStream_t stream);
 
 /*
  * ft_moe_combine -- out[t] = sum_{j<k} topk_w[t, j] * y_rows[row_pos[t*k + j]]

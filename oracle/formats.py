@@ -127,6 +127,10 @@ def expert_to_f64(fmt: str, arrays: dict) -> tuple[np.ndarray, np.ndarray, np.nd
         ts = np.asarray(arrays["tensor_scales"], dtype=np.float32)
         return tuple(nvfp4_to_f64(arrays[f"{n}_codes"], arrays[f"{n}_scales"], ts[i])
                      for i, n in enumerate(("gate", "up", "down")))
+    if fmt == "fp8":
+        from . import fp8
+        return tuple(fp8.to_f64(arrays[f"{n}_codes"], arrays[f"{n}_scales"], fp8.BLOCK)
+                     for n in ("gate", "up", "down"))
     raise ValueError(fmt)
 
 
