@@ -1,5 +1,7 @@
 // ft_fp8_gemm, ft_grouped_gemm and the FP8 experts of ft_moe_grouped_ffn: the
 // entry points and launches of the products in group_gemm.hpp.
+#include <algorithm>
+
 #include "ft_internal.hpp"
 #include "group_gemm.hpp"
 #include "group_ffn.hpp"
@@ -9,16 +11,8 @@ namespace ft {
 template <int TY, int EP, int WM, int WN, int MT, int NT, int STAGES>
 __global__ __launch_bounds__(WM * WN * 64) void group_gemm_kernel(GroupArgs a) {
   using G = GroupTile<TY, EP, WM, WN, MT, NT, STAGES>;
-  // one array per step, so that reads of one do not wait for loads into another
-  __shared__ __attribute__((aligned(16))) uint8_t l0[G::STAGE_BYTES];
-  __shared__ __attribute__((aligned(16))) uint8_t l1[G::STAGE_BYTES];
-  if constexpr (STAGES == 2) {
-    G::run(a, typename G::Ring{{l0, l1}});
-  } else {
-    static_assert(STAGES == 3, "two or three steps");
-    __shared__ __attribute__((aligned(16))) uint8_t l2[G::STAGE_BYTES];
-    G::run(a, typename G::Ring{{l0, l1, l2}});
-  }
+  __shared__ __attribute__((aligned(16))) uint8_t ring[STAGES * G::STAGE_BYTES];
+  G::run(a, ring);
 }
 
 // Most row tiles that the groups can have.
@@ -39,15 +33,41 @@ static ft_status launch_tiles(GroupArgs a, hipStream_t stream) {
   return FT_OK;
 }
 
-template <int TY>
-static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
-  return launch_tiles<TY, GE_OUT, 2, 2, 2, 2, 3>(a, stream);
+// Tile sizes.  256 x 256 (two steps in the ring, 132 KiB of LDS) moves the
+// fewest operand bytes per product; 128 x 256 has room for three steps, which
+// counts where the groups are short and the weights come from HBM; 64 x 64
+// fills the chip when there are few rows.  Measured, 256 / 128 / 64 rows a
+// tile: dense 8192 x 4096 x 4096 FP8 134 / 160 / 257 us; FP8 groups of 192 rows
+// on average (256 groups, N = K = 4096) 1.35 / 1.35 / 2.2 ms; the FP8 experts
+// with 96 rows on average 2.02 / 1.78 / 2.19 ms; bf16 groups of 256 rows
+// (N 2048, K 768) 201 / 210 / 285 us.
+enum { TILE_64, TILE_128, TILE_256 };
+static int tile_choice(const GroupArgs &a, int cols256) {
+  const int groups = a.offsets != nullptr ? std::min(a.E, a.rows) : 1;
+  const int mean = a.rows / std::max(1, groups);
+  auto tiles = [&](int BM) {
+    return (a.offsets != nullptr ? a.rows / BM + groups / 2 : cdiv(a.rows, BM)) * int64_t(cdiv(a.N, cols256));
+  };
+  if (mean >= 160 && tiles(256) >= 224) return TILE_256;
+  if (mean >= 24 && tiles(128) >= 192) return TILE_128;
+  return TILE_64;
 }
 
-static ft_status group_products(int dtype, const GroupArgs &a, hipStream_t stream) {
+template <int TY, int EP>
+static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
+  constexpr bool GLU = EP == GE_GLU;
+  switch (tile_choice(a, GLU ? 128 : 256)) {
+    case TILE_256: return launch_tiles<TY, EP, 2, 4, 8, 4, 2>(a, stream);
+    case TILE_128: return launch_tiles<TY, EP, 2, 4, 4, 4, 3>(a, stream);
+    default: return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
+  }
+}
+
+static ft_status group_products(int dtype, int out_dtype, const GroupArgs &a, hipStream_t stream) {
   if (a.rows == 0 || a.N == 0) return FT_OK;
-  if (dtype == FT_BF16) return launch_products<GT_BF16>(a, stream);
-  return a.out_bf16 ? launch_products<GT_FP8>(a, stream) : launch_products<GT_FP8X>(a, stream);
+  if (dtype == FT_BF16)
+    return out_dtype == FT_BF16 ? launch_products<GT_BF16, GE_BF16>(a, stream) : launch_products<GT_BF16, GE_F32>(a, stream);
+  return out_dtype == FT_BF16 ? launch_products<GT_FP8, GE_BF16>(a, stream) : launch_products<GT_FP8X, GE_F32>(a, stream);
 }
 
 // ------------------------------------------------------------------ FP8 experts
@@ -108,7 +128,7 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
     g.a_rows = f.T;
     g.out = ws + W.h;
     g.ldo = I;
-    if ((st = launch_tiles<GT_FP8, GE_GLU, 2, 2, 2, 4, 3>(g, stream)) != FT_OK) return st;
+    if ((st = launch_products<GT_FP8, GE_GLU>(g, stream)) != FT_OK) return st;
   }
   if (f.down) {
     st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, reinterpret_cast<float *>(ws + W.hs), stream);
@@ -127,7 +147,7 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
     d.out = f.y_rows;
     d.ldo = H;
     d.out_shared = f.y_shared;
-    if ((st = launch_tiles<GT_FP8, GE_OUT, 2, 2, 2, 2, 3>(d, stream)) != FT_OK) return st;
+    if ((st = launch_products<GT_FP8, GE_F32>(d, stream)) != FT_OK) return st;
   }
   return FT_OK;
 }
@@ -172,9 +192,8 @@ extern "C" ft_status ft_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_s
   g.k = 1;
   g.a_rows = M;
   g.out = out;
-  g.out_bf16 = out_dtype == FT_BF16;
   g.ldo = ldo;
-  const ft_status st = group_products(FT_FP8, g, stream);
+  const ft_status st = group_products(FT_FP8, out_dtype, g, stream);
   if (st != FT_OK) return st;
   clear_error();
   return FT_OK;
@@ -236,9 +255,8 @@ extern "C" ft_status ft_grouped_gemm(int32_t dtype, const void *a, int64_t lda, 
   g.sorted_rows = sorted_rows;
   g.a_rows = sorted_rows != nullptr ? T : int64_t(T) * k;
   g.out = out;
-  g.out_bf16 = out_dtype == FT_BF16;
   g.ldo = ldo;
-  const ft_status st = group_products(dtype, g, stream);
+  const ft_status st = group_products(dtype, out_dtype, g, stream);
   if (st != FT_OK) return st;
   clear_error();
   return FT_OK;

@@ -9,7 +9,8 @@
 // A tile is BM rows of one group by BN weight rows; a step is 128 bytes of the
 // contraction axis, i.e. 64 bf16 elements or one FP8 scale block.  Both
 // operands of a step are copied into LDS by direct loads (lane i of a load
-// writes 16 bytes at base + 16 i), STAGES steps in a ring.  A row of a step is
+// writes 16 bytes at base + 16 i), STAGES steps in a ring, while earlier ones
+// are multiplied.  A row of a step is
 // 128 bytes; its 16-byte chunk j sits in slot j ^ ((row / 2) % 8), so that the
 // 16 rows an MFMA operand reads fall into distinct banks.
 //
@@ -42,7 +43,10 @@
 namespace ft {
 
 enum { GT_BF16 = 0, GT_FP8 = 1, GT_FP8X = 2 };  // operand type / instruction
-enum { GE_OUT = 0, GE_GLU = 1 };                // epilogue: the products; silu(gate) * up (fp32)
+enum { GE_F32 = 0, GE_BF16 = 1, GE_GLU = 2 };   // outputs: the products in fp32 or bf16; silu(gate) * up in fp32
+
+// lambdas that hold register arrays: a call would put those into memory
+#define FT_INLINE __attribute__((always_inline))
 
 constexpr int kStepBytes = 128;  // bytes of the contraction axis per step
 
@@ -67,10 +71,9 @@ struct GroupArgs {
   int64_t a_rows;                 // rows of A that sorted_rows may name
   int a_shared0;                  // first A row of the shared group
   void *out;
-  int out_bf16;
   int64_t ldo;                    // elements
   float *out_shared;              // rows of the shared group (NULL: behind the others in out)
-  int n_ntiles, n_mtiles;
+  int n_ntiles;
 };
 
 // Rows of group e: first row and count, held inside [0, rows] whatever the offsets say.
@@ -96,12 +99,21 @@ struct GroupItem {
   int m;     // rows of the tile
 };
 
-// This workgroup's tile.  Tiles are group-major and weight-tile major within a
-// group (the row tiles of one weight tile are neighbours), and each XCD takes a
-// contiguous range of those present: a group's rows and weights then sit in
-// one XCD's L2.  Block ids go round robin over the 8 XCDs.
+// This workgroup's tile.  Tiles are group-major; a group's tiles come in columns
+// of kColumn weight tiles, row tile by row tile.  Each XCD takes a contiguous
+// range of those present (block ids go round robin over the 8 XCDs), so what
+// runs on one XCD at a time is a block of a few row tiles by kColumn weight
+// tiles, and its L2 serves every operand byte several times.
+constexpr int kColumn = 8;
+
+__device__ __forceinline__ void tile_of(int local, int tiles, int NT, int *nt, int *mt) {
+  const int c = local / (tiles * kColumn), rest = local - c * tiles * kColumn, w = min(kColumn, NT - c * kColumn);
+  *mt = rest / w;
+  *nt = c * kColumn + rest % w;
+}
+
 template <int THREADS, int BM>
-__device__ bool group_item(const GroupArgs &a, GroupItem *it) {
+__device__ __forceinline__ bool group_item(const GroupArgs &a, GroupItem *it) {
   constexpr int NW = THREADS / 64;
   __shared__ int s_cnt[NW];
   __shared__ int s_hit[4];
@@ -130,10 +142,11 @@ __device__ bool group_item(const GroupArgs &a, GroupItem *it) {
   if (b / 8 >= per || item >= n_items) return false;
   if (item >= total * NT) {
     const int local = item - total * NT;
-    it->nt = local / shared_tiles;
+    int mt;
+    tile_of(local, shared_tiles, NT, &it->nt, &mt);
     it->e = a.E;
     it->lo = 0;
-    it->row0 = (local % shared_tiles) * BM;
+    it->row0 = mt * BM;
     it->m = min(BM, a.T - it->row0);
     return true;
   }
@@ -165,14 +178,40 @@ __device__ bool group_item(const GroupArgs &a, GroupItem *it) {
   it->lo = __builtin_amdgcn_readfirstlane(s_hit[1]);
   const int m = __builtin_amdgcn_readfirstlane(s_hit[2]), local = __builtin_amdgcn_readfirstlane(s_hit[3]);
   const int tiles = (m + BM - 1) / BM;
-  it->nt = local / tiles;
-  it->row0 = (local % tiles) * BM;
+  int mt;
+  tile_of(local, tiles, NT, &it->nt, &mt);
+  it->row0 = mt * BM;
   it->m = min(BM, m - it->row0);
   return true;
 }
 
-__device__ __forceinline__ void lds_load16(rsrc_t r, uint8_t *dst, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
+// Lane `lane`'s value, to every lane.
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// Direct loads: lane i's 16 (4) bytes at base + off + step go to LDS address
+// dst + 16 i (4 i).  Written as assembly, without outputs, because the compiler
+// cannot tell one step's buffer from another's when the ring's position is a
+// run-time value: it would wait for all loads in flight before every LDS read.
+// The kernel counts them itself (wait_vmcnt before the barrier that publishes
+// a step); the compiler's own waits only see fewer loads than there are, so
+// they wait for more.
+__device__ __forceinline__ void lds_load16(u32x4 r, uint32_t dst, uint32_t off, uint32_t step) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(off), "s"(r), "s"(dst), "s"(step)
+               : "memory");
+}
+__device__ __forceinline__ void lds_load4(u32x4 r, uint32_t dst, uint32_t off, uint32_t step) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %3 offen lds" ::"v"(off), "s"(r), "s"(dst), "s"(step)
+               : "memory");
+}
+// The descriptor of make_rsrc as four scalar words.
+__device__ __forceinline__ u32x4 rsrc_words(const void *base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return u32x4{uint32_t(p), uint32_t(p >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
 
 template <int TY, int EP, int WM, int WN, int MT, int NT, int STAGES>
@@ -186,11 +225,15 @@ struct GroupTile {
   static constexpr int STAGE_BYTES = (BM + BN) * kStepBytes + (FP8 ? WAVES * 256 : 0);
   static_assert(AL >= 1 && WL >= 1 && AL * WAVES * 8 == BM && WL * WAVES * 8 == BN, "whole direct loads");
   static_assert(NT % 2 == 0 && (EP != GE_GLU || (NT == 4 && WL * 8 <= 32 && 32 % (WL * 8) == 0)), "tile pairs");
-  static_assert(BM / WAVES <= 32 && NCOL <= 4096, "scale slots");
+  static_assert(BM / WAVES <= 64, "one row scale per lane");
 
-  struct Ring {
-    uint8_t *b[STAGES];
-  };
+
+  // First of the loads that go with row tile i of mtr: evenly over the tiles, or
+  // over the first half of them where the ring holds only one step ahead
+  static constexpr int load_at(int i, int mtr) {
+    const int n = i * LOADS * (STAGES == 2 ? 2 : 1) / mtr;
+    return n < LOADS ? n : LOADS;
+  }
 
   // Output of weight row p of the tile's LDS order, relative to the tile's first:
   // pairs of 16-row tiles are interleaved by 4 so that a lane's two
@@ -202,17 +245,18 @@ struct GroupTile {
   }
 
   template <int MTR>
-  static __device__ __forceinline__ void body(const GroupArgs &a, const Ring &L, const GroupItem &it, const uint8_t *blob) {
+  static __device__ __forceinline__ void body(const GroupArgs &a, uint8_t *L, const GroupItem &it, const uint8_t *blob) {
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int r = lane & 15, q = lane >> 4, wm = wave % WM, wn = wave / WM;
     const bool shared = it.e == a.E;
     const int n0 = it.nt * NCOL;
     const int nk = cdiv(a.Kb, kStepBytes);
 
-    // ---- sources of the direct loads
+    // ---- sources of the direct loads: a lane's offset inside its operand is
+    // fixed, the step is the instruction's scalar offset
     const bool gather = a.sorted_rows != nullptr && !shared;
     const int64_t a_first = gather ? 0 : int64_t(shared ? a.a_shared0 : it.lo) + it.row0;
-    const rsrc_t ares = make_rsrc(a.A + a_first * a.lda, uint32_t(((gather ? a.a_rows : it.m) - 1) * a.lda + a.Kb));
+    const int64_t a_count = gather ? a.a_rows : it.m;
     // A row of the tile's row rr, relative to a_first; -1: none
     auto a_row = [&](int rr) -> int {
       if (rr >= it.m) return -1;
@@ -220,53 +264,78 @@ struct GroupTile {
       const uint32_t s = uint32_t(a.sorted_rows[it.lo + it.row0 + rr]) / uint32_t(a.k);
       return s < uint32_t(a.a_rows) ? int(s) : -1;  // a negative entry: above every token
     };
+    const uint8_t *abase = a.A + a_first * a.lda;
+    const uint32_t abytes = uint32_t((a_count - 1) * a.lda + a.Kb);
+    const bool up = EP == GE_GLU && ((wave * WL * 8) % (NT * 16)) >= 32;
+    const uint8_t *wbase = blob + (up ? a.off_w1 : a.off_w0) + uint64_t(n0) * uint64_t(a.ldw);
+    const uint32_t wbytes = uint32_t((min(NCOL, a.N - n0) - 1) * a.ldw + a.Kb);
     uint32_t aoff[AL], woff[WL];
-    int abyte[AL], wbyte[WL];
 #pragma unroll
     for (int t = 0; t < AL; ++t) {
       const int rr = (wave * AL + t) * 8 + (lane >> 3), src = a_row(rr);
-      abyte[t] = ((lane & 7) ^ ((rr >> 1) & 7)) * 16;
-      aoff[t] = src >= 0 ? uint32_t(src) * uint32_t(a.lda) + uint32_t(abyte[t]) : kOOB;
+      aoff[t] = src >= 0 ? uint32_t(src) * uint32_t(a.lda) + uint32_t(((lane & 7) ^ ((rr >> 1) & 7)) * 16) : kOOB;
     }
-    const bool up = EP == GE_GLU && ((wave * WL * 8) % (NT * 16)) >= 32;
-    const rsrc_t wres = make_rsrc(blob + (up ? a.off_w1 : a.off_w0) + uint64_t(n0) * uint64_t(a.ldw),
-                                  uint32_t((min(NCOL, a.N - n0) - 1) * a.ldw + a.Kb));
 #pragma unroll
     for (int t = 0; t < WL; ++t) {
       const int p = (wave * WL + t) * 8 + (lane >> 3), n = col_of(p);
-      wbyte[t] = ((lane & 7) ^ ((p >> 1) & 7)) * 16;
-      woff[t] = n0 + n < a.N ? uint32_t(n) * uint32_t(a.ldw) + uint32_t(wbyte[t]) : kOOB;
+      woff[t] = n0 + n < a.N ? uint32_t(n) * uint32_t(a.ldw) + uint32_t(((lane & 7) ^ ((p >> 1) & 7)) * 16) : kOOB;
     }
-    // scales: lanes 0..31 of a wave take the rows it loads, lanes 32.. the
-    // weights' blocks of the tile (GLU: gate's, then up's); the others reread
-    // a value that is there
-    constexpr int NSB = (NCOL + 127) / 128;
-    const float *sp = nullptr;
-    if constexpr (FP8) {
-      const float *sw = reinterpret_cast<const float *>(blob + a.off_s0);
-      sp = sw;
-      if (lane < 32) {
-        const int rr = wave * (BM / WAVES) + lane, src = lane < BM / WAVES ? a_row(rr) : -1;
-        if (src >= 0) sp = a.As + (a_first + src) * a.KB;
-      } else {
-        const int u = lane - 32, mat = u / NSB, nb = n0 / 128 + u % NSB;
-        if (mat == 1 && EP == GE_GLU) sw = reinterpret_cast<const float *>(blob + a.off_s1);
-        if (mat < (EP == GE_GLU ? 2 : 1) && nb < cdiv(a.N, 128)) sp = sw + int64_t(nb) * a.KB;
-      }
-    }
-    auto load = [&](int c, uint8_t *buf) {
-      const uint32_t at = uint32_t(c) * kStepBytes;
+    // the last step of a K that is no multiple of 128 bytes: chunks past it load zeros
+    const int tail = a.Kb % kStepBytes;
+    auto cut = [&]() {
 #pragma unroll
       for (int t = 0; t < AL; ++t)
-        lds_load16(ares, buf + (wave * AL + t) * 1024, int(at) + abyte[t] < a.Kb ? aoff[t] + (aoff[t] == kOOB ? 0u : at) : kOOB);
+        if (((lane & 7) ^ ((((wave * AL + t) * 8 + (lane >> 3)) >> 1) & 7)) * 16 >= tail) aoff[t] = kOOB;
 #pragma unroll
       for (int t = 0; t < WL; ++t)
-        lds_load16(wres, buf + BM * kStepBytes + (wave * WL + t) * 1024,
-                   int(at) + wbyte[t] < a.Kb ? woff[t] + (woff[t] == kOOB ? 0u : at) : kOOB);
-      if constexpr (FP8)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void *)(sp + min(c, a.KB - 1)),
-            (__attribute__((address_space(3))) void *)(buf + (BM + BN) * kStepBytes + wave * 256), 4, 0, 0);
+        if (((lane & 7) ^ ((((wave * WL + t) * 8 + (lane >> 3)) >> 1) & 7)) * 16 >= tail) woff[t] = kOOB;
+    };
+    // row scales: the lanes of a wave take the rows that it loads, one value per
+    // step.  Weight scales are one value per step for the whole wave (GLU: per
+    // matrix): lane l holds those of 64 steps, and a step reads its lane.
+    uint32_t soff = kOOB;
+    const float *swp0 = nullptr, *swp1 = nullptr;
+    if constexpr (FP8) {
+      const int src = lane < BM / WAVES ? a_row(wave * (BM / WAVES) + lane) : -1;
+      if (src >= 0) soff = uint32_t(src) * uint32_t(a.KB) * 4u;
+      const int nb = min((n0 + wn * (EP == GE_GLU ? 32 : NT * 16)) / 128, cdiv(a.N, 128) - 1);
+      swp0 = reinterpret_cast<const float *>(blob + a.off_s0) + int64_t(nb) * a.KB;
+      if (EP == GE_GLU) swp1 = reinterpret_cast<const float *>(blob + a.off_s1) + int64_t(nb) * a.KB;
+    }
+    // Tiles start at different steps (within 2 KB of each other's columns) and
+    // wrap around: side by side on one XCD, they would all ask the same L2
+    // channels at once (dense 8192 x 4096 x 4096: 137 -> 134 us).
+    const int first = tail == 0 ? (it.nt + it.row0 / BM + it.e) % min(16, nk) : 0;
+    auto step_of = [&](int c) { return c + first < nk ? c + first : c + first - nk; };
+    const float *sbase = FP8 ? a.As + a_first * a.KB : nullptr;
+    const uint32_t ldsb = __builtin_amdgcn_readfirstlane(lds_address(L));
+    // Step c's loads, into the ring at byte `at`.  A step past the end loads
+    // nothing (empty buffers, so that every step has the same instructions in
+    // flight).
+    struct Loads {
+      u32x4 ares, wres, sres;
+      uint32_t at, st, ss;
+    };
+    auto plan = [&](int c, uint32_t at) FT_INLINE {
+      const bool live = c < nk;
+      if (tail != 0 && c == nk - 1) cut();
+      const int ks = step_of(c);
+      Loads l;
+      l.at = ldsb + at;
+      l.st = live ? uint32_t(ks) * kStepBytes : 0u;
+      l.ss = live ? uint32_t(ks) * 4u : 0u;
+      l.ares = rsrc_words(abase, live ? abytes : 0u);
+      l.wres = rsrc_words(wbase, live ? wbytes : 0u);
+      if constexpr (FP8) l.sres = rsrc_words(sbase, live ? uint32_t(a_count * a.KB * 4) : 0u);
+      return l;
+    };
+    auto load = [&](const Loads &l, int t) FT_INLINE {  // the t-th of them, 0 .. LOADS - 1
+      if (t < WL)
+        lds_load16(l.wres, l.at + BM * kStepBytes + (wave * WL + t) * 1024, woff[t], l.st);
+      else if (t < WL + AL)
+        lds_load16(l.ares, l.at + (wave * AL + t - WL) * 1024, aoff[t - WL], l.st);
+      else
+        lds_load4(l.sres, l.at + (BM + BN) * kStepBytes + wave * 256, soff, l.ss);
     };
 
     f32x4 acc[MTR][NT];
@@ -278,72 +347,112 @@ struct GroupTile {
     const int sw = (r >> 1) & 7;
     const int lo16 = r * kStepBytes + ((q ^ sw) << 4), hi16 = r * kStepBytes + (((4 + q) ^ sw) << 4);
 
-    auto compute = [&](const uint8_t *buf) {
+    constexpr int kScaleSteps = 64;
+    float swv0 = 0.f, swv1 = 0.f;
+    int sw_first = 0;
+    auto load_weight_scales = [&](int c) {
+      sw_first = c;
+      const int b = step_of(min(c + lane, nk - 1));
+      swv0 = swp0[b];
+      if (EP == GE_GLU) swv1 = swp1[b];
+    };
+
+    // ---- operands of one step: the weights' in registers for the whole step, the
+    // rows' one tile ahead of its products
+    struct Frag {
+      u32x4 wl[NT], wh[NT], al[2], ah[2];
+      float sa[2];
+    };
+    Frag f;
+    auto read_w = [&](const uint8_t *buf) FT_INLINE {
       const uint8_t *wb = buf + (BM + wn * NT * 16) * kStepBytes;
-      u32x4 wl[NT], wh[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        wl[j] = *reinterpret_cast<const u32x4 *>(wb + j * 16 * kStepBytes + lo16);
-        wh[j] = *reinterpret_cast<const u32x4 *>(wb + j * 16 * kStepBytes + hi16);
+        f.wl[j] = *reinterpret_cast<const u32x4 *>(wb + j * 16 * kStepBytes + lo16);
+        f.wh[j] = *reinterpret_cast<const u32x4 *>(wb + j * 16 * kStepBytes + hi16);
       }
-      const float *sc = reinterpret_cast<const float *>(buf + (BM + BN) * kStepBytes);
-      // this wave's weight scales: one for all its columns (GLU: one per matrix)
+    };
+    auto read_a = [&](int i, const uint8_t *buf) FT_INLINE {
+      const uint8_t *ab = buf + (i * WM + wm) * 16 * kStepBytes;
+      f.al[i & 1] = *reinterpret_cast<const u32x4 *>(ab + lo16);
+      f.ah[i & 1] = *reinterpret_cast<const u32x4 *>(ab + hi16);
+      if constexpr (FP8) {
+        const float *sc = reinterpret_cast<const float *>(buf + (BM + BN) * kStepBytes);
+        const int row = (i * WM + wm) * 16 + r;
+        f.sa[i & 1] = sc[row / (BM / WAVES) * 64 + row % (BM / WAVES)];
+      }
+    };
+    // The products of step c, and the loads of a later step among them: issued
+    // in one go, they would hold up the wave (a CU takes 64 bytes of load a
+    // clock, so a step's loads take about as long as its products).  FP8
+    // additions follow the products they add; the SIMD's other wave multiplies
+    // meanwhile.
+    auto compute = [&](int c, const uint8_t *buf, const Loads &next) FT_INLINE {
       float sw0 = 0.f, sw1 = 0.f;
       if constexpr (FP8) {
-        const int nb = EP == GE_GLU ? (n0 + wn * 32) / 128 - n0 / 128 : (n0 + wn * NT * 16) / 128 - n0 / 128;
-        sw0 = sc[wave * 64 + 32 + nb];
-        if (EP == GE_GLU) sw1 = sc[wave * 64 + 32 + NSB + nb];
+        sw0 = lane_value(swv0, c - sw_first);
+        if (EP == GE_GLU) sw1 = lane_value(swv1, c - sw_first);
       }
+      read_a(0, buf);
+      read_w(buf);
 #pragma unroll
       for (int i = 0; i < MTR; ++i) {
-        const uint8_t *ab = buf + (i * WM + wm) * 16 * kStepBytes;
-        const u32x4 al = *reinterpret_cast<const u32x4 *>(ab + lo16), ah = *reinterpret_cast<const u32x4 *>(ab + hi16);
-        if constexpr (!FP8) {
+        if (i + 1 < MTR) read_a(i + 1, buf);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            acc[i][j] = mfma16(as_bf16x8(wl[j]), as_bf16x8(al), acc[i][j]);
-            acc[i][j] = mfma16(as_bf16x8(wh[j]), as_bf16x8(ah), acc[i][j]);
-          }
-        } else {
-          const int row = (i * WM + wm) * 16 + r;
-          const float sa = sc[row / (BM / WAVES) * 64 + row % (BM / WAVES)];
-          const float s0 = sa * sw0, s1 = EP == GE_GLU ? sa * sw1 : s0;
+        for (int t = load_at(i, MTR); t < load_at(i + 1, MTR); ++t) load(next, t);
+        const u32x4 xl = f.al[i & 1], xh = f.ah[i & 1];
+        f32x4 p[NT];
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            f32x4 p = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (TY == GT_FP8) {
-              p = fp8_mfma(wl[j], wh[j], al, ah);
-            } else {
-              p = fp8x_mfma(wl[j], al, p);
-              p = fp8x_mfma(wh[j], ah, p);
-            }
-            const float s = EP == GE_GLU && j >= NT / 2 ? s1 : s0;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], s, acc[i][j][v]);
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (!FP8) {
+            acc[i][j] = mfma16(as_bf16x8(f.wl[j]), as_bf16x8(xl), acc[i][j]);
+            acc[i][j] = mfma16(as_bf16x8(f.wh[j]), as_bf16x8(xh), acc[i][j]);
+          } else if constexpr (TY == GT_FP8) {
+            p[j] = fp8_mfma(f.wl[j], f.wh[j], xl, xh);
+          } else {
+            p[j] = fp8x_mfma(f.wh[j], xh, fp8x_mfma(f.wl[j], xl, f32x4{0.f, 0.f, 0.f, 0.f}));
           }
         }
+        if constexpr (FP8) {
+          const float s0 = f.sa[i & 1] * sw0, s1 = EP == GE_GLU ? f.sa[i & 1] * sw1 : s0;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const float s = EP == GE_GLU && j >= NT / 2 ? s1 : s0;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[j][v], s, acc[i][j][v]);
+          }
+        }
+        // here, and not behind the products of all row tiles, which would all stay live
+#pragma unroll
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // ---- a ring of STAGES steps: at step c the loads of step c have landed
-    // and every wave is done with step c - 1, whose buffer takes step
-    // c + STAGES - 1
+    // ---- a ring of STAGES steps: at turn c the loads of step c have landed and
+    // every wave is done with step c - 1, whose buffer takes step c + STAGES - 1
+    if constexpr (FP8) {
+      load_weight_scales(0);
+      wait_vmcnt<0>();
+    }
 #pragma unroll
     for (int p = 0; p < STAGES - 1; ++p) {
-      load(p, L.b[p]);
-      __builtin_amdgcn_sched_barrier(0);
+      const Loads l = plan(p, p * STAGE_BYTES);
+#pragma unroll
+      for (int t = 0; t < LOADS; ++t) load(l, t);
     }
-    auto step = [&](auto jc, int c) {
-      constexpr int J = decltype(jc)::value;
-      if (c >= nk) return;
+    uint32_t at = 0, put = (STAGES - 1) * STAGE_BYTES;  // of step c, of step c + STAGES - 1
+    for (int c = 0; c < nk; ++c) {
+      if (FP8 && c - sw_first == kScaleSteps) {
+        load_weight_scales(c);
+        wait_vmcnt<0>();
+      }
       wait_vmcnt<(STAGES - 2) * LOADS>();
       lds_barrier();
-      load(c + STAGES - 1, L.b[(J + STAGES - 1) % STAGES]);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(L.b[J]);
-    };
-    for (int c = 0; c < nk; c += STAGES)
-      unroll_steps([&](auto jc) { step(jc, c + decltype(jc)::value); }, std::make_integer_sequence<int, STAGES>{});
+      compute(c, L + at, plan(c + STAGES - 1, put));
+      at = at == (STAGES - 1) * STAGE_BYTES ? 0 : at + STAGE_BYTES;
+      put = put == (STAGES - 1) * STAGE_BYTES ? 0 : put + STAGE_BYTES;
+    }
     wait_vmcnt<0>();
 
     // ---- epilogue
@@ -362,20 +471,16 @@ struct GroupTile {
         }
         store8(o, n, a.N, v, a.ldo % 4 == 0);
       } else {
-        const bool own = shared && a.out_shared != nullptr;
-        const int64_t orow = own ? it.row0 + rr : int64_t(shared ? a.rows : it.lo) + it.row0 + rr;
+        using O = std::conditional_t<EP == GE_BF16, uint16_t, float>;
+        const bool own = EP == GE_F32 && shared && a.out_shared != nullptr;
+        O *o = own ? reinterpret_cast<O *>(a.out_shared) + int64_t(it.row0 + rr) * a.ldo
+                   : static_cast<O *>(a.out) + (int64_t(shared ? a.rows : it.lo) + it.row0 + rr) * a.ldo;
 #pragma unroll
         for (int jj = 0; jj < NT / 2; ++jj) {
-          const int n = n0 + wn * NT * 16 + 32 * jj + 8 * q;
           float v[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) v[u] = acc[i][2 * jj + u / 4][u % 4];
-          if (own)
-            store8(a.out_shared + orow * a.ldo, n, a.N, v, a.ldo % 4 == 0);
-          else if (a.out_bf16)
-            store8(static_cast<uint16_t *>(a.out) + orow * a.ldo, n, a.N, v, a.ldo % 8 == 0);
-          else
-            store8(static_cast<float *>(a.out) + orow * a.ldo, n, a.N, v, a.ldo % 4 == 0);
+          store8(o, n0 + wn * NT * 16 + 32 * jj + 8 * q, a.N, v, a.ldo % (16 / sizeof(O)) == 0);
         }
       }
     }
@@ -418,24 +523,19 @@ struct GroupTile {
       if (n + u < N) o[n + u] = uint16_t(d[u / 2] >> (16 * (u & 1)));
   }
 
-  template <typename F, int... J>
-  static __device__ __forceinline__ void unroll_steps(F &&f, std::integer_sequence<int, J...>) {
-    (f(std::integral_constant<int, J>{}), ...);
-  }
-
   // The rows of a group whose weights are not resident.
   static __device__ __forceinline__ void fill_nan(const GroupArgs &a, const GroupItem &it) {
     const int n0 = it.nt * NCOL, w = min(NCOL, a.N - n0);
     for (int u = threadIdx.x; u < it.m * w; u += THREADS) {
       const int64_t at = (int64_t(it.lo) + it.row0 + u / w) * a.ldo + n0 + u % w;
-      if (EP == GE_OUT && a.out_bf16)
+      if (EP == GE_BF16)
         static_cast<uint16_t *>(a.out)[at] = 0x7fc0;
       else
         static_cast<float *>(a.out)[at] = __builtin_nanf("");
     }
   }
 
-  static __device__ __forceinline__ void run(const GroupArgs &a, const Ring &L) {
+  static __device__ __forceinline__ void run(const GroupArgs &a, uint8_t *L) {
     GroupItem it;
     if (!group_item<THREADS, BM>(a, &it)) return;
     const uint8_t *blob = a.shared_blob;
@@ -454,8 +554,10 @@ struct GroupTile {
       if (mt > 6) return body<8>(a, L, it, blob);
       if (mt > 4) return body<6>(a, L, it, blob);
     }
-    if constexpr (MT >= 4)
-      if (mt > 2) return body<4>(a, L, it, blob);
+    if constexpr (MT >= 4) {
+      if (mt > 3) return body<4>(a, L, it, blob);
+      if (mt > 2) return body<3>(a, L, it, blob);
+    }
     if constexpr (MT >= 2)
       if (mt > 1) return body<2>(a, L, it, blob);
     body<1>(a, L, it, blob);

@@ -128,7 +128,8 @@ def test_quantize_bad_blocks(ops):
 
 GEMM = [(1, 1, 16), (1, 16, 128), (1, 4096, 4096), (2, 100, 144), (5, 129, 1040), (16, 64, 128), (17, 200, 400), (33, 1001, 2000),
         (64, 256, 768), (65, 130, 272), (100, 128, 128), (128, 512, 512), (200, 77, 656), (255, 257, 384), (256, 256, 1024),
-        (300, 520, 4096), (513, 300, 112), (1030, 640, 896)]
+        (300, 520, 4096), (513, 300, 112), (1030, 640, 896), (70, 100, 8400), (1000, 6200, 400), (1000, 6200, 8352),
+        (3600, 4100, 272), (3600, 4100, 8320)]
 
 
 @pytest.mark.parametrize("out", [BF16, F32])
@@ -242,7 +243,8 @@ GROUPED = [  # T, k, E, N, K, gather, pad
     (1, 1, 1, 16, 16, True, 0), (1, 2, 4, 100, 144, True, 16), (3, 2, 5, 64, 128, False, 0), (5, 6, 40, 96, 256, True, 0),
     (16, 4, 8, 130, 400, True, 32), (64, 8, 16, 256, 512, True, 0), (33, 3, 300, 48, 64, False, 16), (100, 2, 3, 257, 272, False, 0),
     (130, 2, 2, 64, 1024, True, 0), (600, 1, 4, 300, 336, False, 0), (700, 4, 7, 128, 192, True, 16), (1500, 2, 5, 520, 768, True, 0),
-    (64, 1, 1, 512, 2048, False, 0), (40, 2, 3, 80, 4352, True, 0),
+    (64, 1, 1, 512, 2048, False, 0), (40, 2, 3, 80, 4352, True, 0), (130, 1, 2, 90, 12304, True, 0), (1500, 2, 20, 2100, 208, True, 0),
+    (4000, 3, 12, 1500, 336, True, 16), (4000, 3, 12, 1500, 768, False, 0),
 ]
 
 
@@ -387,7 +389,8 @@ def layer_case(rng, T, k, E, H, I, shared):
 
 
 FFN = [(1, 2, 4, 256, 128, False), (1, 6, 16, 512, 256, True), (3, 2, 5, 208, 144, True), (5, 4, 8, 384, 272, False), (17, 3, 8, 256, 384, True),
-       (64, 8, 16, 512, 128, False), (90, 4, 6, 272, 208, True), (300, 2, 3, 384, 256, True), (700, 2, 4, 256, 144, False)]
+       (64, 8, 16, 512, 128, False), (90, 4, 6, 272, 208, True), (300, 2, 3, 384, 256, True), (700, 2, 4, 256, 144, False),
+       (700, 4, 16, 144, 1040, True), (6000, 2, 4, 128, 1040, True)]
 
 
 @pytest.mark.parametrize("T,k,E,H,I,shared", FFN)
