@@ -1,10 +1,12 @@
 // ft_fp8_gemm, ft_grouped_gemm and the FP8 experts of ft_moe_grouped_ffn: the
 // entry points and launches of the products in group_gemm.hpp.
 #include <algorithm>
+#include <cstdlib>
 
 #include "ft_internal.hpp"
 #include "group_gemm.hpp"
 #include "group_ffn.hpp"
+#include "group_stream.hpp"
 
 namespace ft {
 
@@ -33,6 +35,68 @@ static ft_status launch_tiles(GroupArgs a, hipStream_t stream) {
   return FT_OK;
 }
 
+template <int TY, int EP, int GX, int WAVES, int BPW>
+__global__ __launch_bounds__(WAVES * 64) void group_stream_kernel(GroupArgs a) {
+  using G = GroupStream<TY, EP, GX, WAVES, BPW>;
+  __shared__ typename G::Lds s;
+  G::run(a, s);
+}
+
+// Most sets of up to 16 rows that the groups can have.
+static int row_sets(const GroupArgs &a) {
+  if (a.offsets == nullptr) return cdiv(a.rows, 16);
+  return a.rows / 16 + std::min(a.E, a.rows) + (a.shared_blob != nullptr ? cdiv(a.T, 16) : 0);
+}
+
+// Workgroups of a kernel that the chip holds at once.
+template <typename K>
+static int resident(K kernel, int threads) {
+  int dev = 0, cus = 0, per = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
+    cus = 256;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, reinterpret_cast<const void *>(kernel), threads, 0) != hipSuccess ||
+      per <= 0)
+    per = 1;
+  (void)hipGetLastError();
+  return cus * per;
+}
+
+template <int TY, int EP, int GX, int WAVES, int BPW>
+static ft_status launch_stream_as(GroupArgs a, hipStream_t stream) {
+  static const int fit = resident(&group_stream_kernel<TY, EP, GX, WAVES, BPW>, WAVES * 64);
+  a.n_ntiles = cdiv(a.N, 16);
+  const int64_t units = int64_t(row_sets(a)) * a.n_ntiles;
+  hipLaunchKernelGGL((group_stream_kernel<TY, EP, GX, WAVES, BPW>), dim3(unsigned(std::min<int64_t>(units, fit))),
+                     dim3(WAVES * 64), 0, stream, a);
+  FT_LAUNCHED("group_stream_kernel");
+  return FT_OK;
+}
+
+static bool stream_covers(const GroupArgs &a) {
+  return a.E <= kStreamMaxE && a.rows <= kStreamMaxRows && (a.shared_blob == nullptr || a.T <= 256) &&
+         int64_t(row_sets(a)) * cdiv(a.N, 16) < (int64_t(1) << 30);
+}
+
+// The stream kernel where 64-column tiles would leave most of the chip idle: it
+// spreads 16-column units over it (one row by 4096 x 4096 FP8: 7.6 against 13.0
+// us; 77 rows by 1001 x 2000 in fp32: 7.5 against 10.2).  With enough tiles the
+// LDS ring keeps more of the weights on their way (64 tokens, 128 experts,
+// bf16: 136 us against 156).
+static bool stream_choice(const GroupArgs &a, int64_t cols) {
+  if (a.rows > (a.offsets != nullptr ? 16 * std::min(a.E, a.rows) : 128)) return false;
+  static const char *e = getenv("FTMOE_ST");
+  return row_tiles(a, 32) * cdiv<int64_t>(cols, 64) < (e ? atoi(e) : 192) && stream_covers(a);
+}
+
+template <int TY, int EP, int GX>
+static ft_status launch_stream(const GroupArgs &a, hipStream_t stream) {
+  const int blocks = cdiv(a.Kb, kStepBytes);
+  if (blocks <= 8) return launch_stream_as<TY, EP, GX, 8, 1>(a, stream);
+  if (blocks <= 16) return launch_stream_as<TY, EP, GX, 8, 2>(a, stream);
+  return launch_stream_as<TY, EP, GX, 8, 4>(a, stream);
+}
+
 // Tile sizes.  256 x 256 (two steps in the ring, 132 KiB of LDS) moves the
 // fewest operand bytes per product; 128 x 256 has room for three steps, which
 // counts where the groups are short and the weights come from HBM; 64 x 64
@@ -41,7 +105,7 @@ static ft_status launch_tiles(GroupArgs a, hipStream_t stream) {
 // on average (256 groups, N = K = 4096) 1.35 / 1.35 / 2.2 ms; the FP8 experts
 // with 96 rows on average 2.02 / 1.78 / 2.19 ms; bf16 groups of 256 rows
 // (N 2048, K 768) 201 / 210 / 285 us.
-enum { TILE_64, TILE_128, TILE_256 };
+enum { TILE_32, TILE_64, TILE_128, TILE_256 };
 static int tile_choice(const GroupArgs &a, int cols256) {
   const int groups = a.offsets != nullptr ? std::min(a.E, a.rows) : 1;
   const int mean = a.rows / std::max(1, groups);
@@ -49,8 +113,8 @@ static int tile_choice(const GroupArgs &a, int cols256) {
     return (a.offsets != nullptr ? a.rows / BM + groups / 2 : cdiv(a.rows, BM)) * int64_t(cdiv(a.N, cols256));
   };
   if (mean >= 160 && tiles(256) >= 224) return TILE_256;
-  if (mean >= 24 && tiles(128) >= 192) return TILE_128;
-  return TILE_64;
+  if (mean >= 24 && tiles(128) >= 100) return TILE_128;
+  return mean > 32 ? TILE_64 : TILE_32;
 }
 
 template <int TY, int EP>
@@ -59,12 +123,20 @@ static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
   switch (tile_choice(a, GLU ? 128 : 256)) {
     case TILE_256: return launch_tiles<TY, EP, 2, 4, 8, 4, 2>(a, stream);
     case TILE_128: return launch_tiles<TY, EP, 2, 4, 4, 4, 3>(a, stream);
-    default: return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
+    case TILE_64: return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
+    default: return launch_tiles<TY, EP, 2, 2, 1, GLU ? 4 : 2, GLU ? 3 : 4>(a, stream);
   }
 }
 
 static ft_status group_products(int dtype, int out_dtype, const GroupArgs &a, hipStream_t stream) {
   if (a.rows == 0 || a.N == 0) return FT_OK;
+  if (stream_choice(a, a.N)) {
+    if (dtype == FT_BF16)
+      return out_dtype == FT_BF16 ? launch_stream<GT_BF16, GE_BF16, GX_SAME>(a, stream)
+                                  : launch_stream<GT_BF16, GE_F32, GX_SAME>(a, stream);
+    return out_dtype == FT_BF16 ? launch_stream<GT_FP8X, GE_BF16, GX_SAME>(a, stream)
+                                : launch_stream<GT_FP8X, GE_F32, GX_SAME>(a, stream);
+  }
   if (dtype == FT_BF16)
     return out_dtype == FT_BF16 ? launch_products<GT_BF16, GE_BF16>(a, stream) : launch_products<GT_BF16, GE_F32>(a, stream);
   return out_dtype == FT_BF16 ? launch_products<GT_FP8, GE_BF16>(a, stream) : launch_products<GT_FP8X, GE_F32>(a, stream);
@@ -109,13 +181,15 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
   a.rows = routed;
   a.T = f.T;
   a.k = f.k;
-  ft_status st;
+  ft_status st = FT_OK;
+  a.N = std::max(H, I);  // (of the larger stage, for the choice)
+  const bool stream_it = stream_choice(a, 2 * int64_t(I));
   if (f.gate_up) {
-    st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, reinterpret_cast<float *>(ws + W.xs), stream);
-    if (st != FT_OK) return st;
+    if (!stream_it) st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, reinterpret_cast<float *>(ws + W.xs), stream);
+    if (!stream_it && st != FT_OK) return st;
     GroupArgs g = a;
-    g.A = ws + W.xq;
-    g.lda = H;
+    g.A = stream_it ? static_cast<const uint8_t *>(f.x) : ws + W.xq;
+    g.lda = stream_it ? 2 * H : H;
     g.As = reinterpret_cast<const float *>(ws + W.xs);
     g.off_w0 = L.off_gate;
     g.off_w1 = L.off_up;
@@ -128,14 +202,15 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
     g.a_rows = f.T;
     g.out = ws + W.h;
     g.ldo = I;
-    if ((st = launch_products<GT_FP8, GE_GLU>(g, stream)) != FT_OK) return st;
+    st = stream_it ? launch_stream<GT_FP8, GE_GLU, GX_BF16>(g, stream) : launch_products<GT_FP8, GE_GLU>(g, stream);
+    if (st != FT_OK) return st;
   }
   if (f.down) {
-    st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, reinterpret_cast<float *>(ws + W.hs), stream);
-    if (st != FT_OK) return st;
+    if (!stream_it) st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, reinterpret_cast<float *>(ws + W.hs), stream);
+    if (!stream_it && st != FT_OK) return st;
     GroupArgs d = a;
-    d.A = ws + W.hq;
-    d.lda = I;
+    d.A = stream_it ? ws + W.h : ws + W.hq;
+    d.lda = stream_it ? 4 * int64_t(I) : I;
     d.As = reinterpret_cast<const float *>(ws + W.hs);
     d.off_w0 = d.off_w1 = L.off_down;
     d.off_s0 = d.off_s1 = L.off_sdown;
@@ -147,7 +222,8 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
     d.out = f.y_rows;
     d.ldo = H;
     d.out_shared = f.y_shared;
-    if ((st = launch_products<GT_FP8, GE_F32>(d, stream)) != FT_OK) return st;
+    st = stream_it ? launch_stream<GT_FP8, GE_F32, GX_F32>(d, stream) : launch_products<GT_FP8, GE_F32>(d, stream);
+    if (st != FT_OK) return st;
   }
   return FT_OK;
 }

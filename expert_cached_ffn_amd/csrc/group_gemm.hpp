@@ -119,20 +119,22 @@ __device__ __forceinline__ bool group_item(const GroupArgs &a, GroupItem *it) {
   __shared__ int s_hit[4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int NT = a.n_ntiles;
-  int total = 0, lo0 = 0, m0 = 0;
-  for (int c0 = 0; c0 < a.E; c0 += THREADS) {
-    int lo = 0;
-    const int m = group_rows(a, c0 + tid, &lo);
-    if (c0 == 0) {
-      lo0 = lo;
-      m0 = m;
-    }
-    const int v = wave_sum_i32((m + BM - 1) / BM);
-    if (lane == 0) s_cnt[wave] = v;
-    __syncthreads();
+  // thread t counts the tiles of groups t * per_thread .. and an exclusive scan
+  // over the threads finds the one whose range holds the item
+  const int per_thread = (a.E + THREADS - 1) / THREADS, e0 = tid * per_thread;
+  int mine = 0;
+  for (int i = 0; i < per_thread; ++i) {
+    int lo;
+    mine += (group_rows(a, e0 + i, &lo) + BM - 1) / BM;
+  }
+  const int incl = wave_incl_scan_i32(mine);
+  if (lane == 63) s_cnt[wave] = incl;
+  __syncthreads();
+  int total = 0, first = incl - mine;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) total += s_cnt[w];
-    __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    if (w < wave) first += s_cnt[w];
+    total += s_cnt[w];
   }
   const int shared_tiles = a.shared_blob != nullptr ? (a.T + BM - 1) / BM : 0;
   const int n_items = (total + shared_tiles) * NT;
@@ -150,30 +152,22 @@ __device__ __forceinline__ bool group_item(const GroupArgs &a, GroupItem *it) {
     it->m = min(BM, a.T - it->row0);
     return true;
   }
-  int base = 0;
-  for (int c0 = 0; c0 < a.E; c0 += THREADS) {
-    int lo = lo0;
-    const int m = c0 == 0 ? m0 : group_rows(a, c0 + tid, &lo);
-    const int tiles = (m + BM - 1) / BM;
-    const int incl = wave_incl_scan_i32(tiles * NT);
-    if (lane == 63) s_cnt[wave] = incl;
-    __syncthreads();
-    int before = base;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      if (w < wave) before += s_cnt[w];
-      base += s_cnt[w];
+  if (item >= first * NT && item < (first + mine) * NT) {
+    int local = item - first * NT;
+    for (int i = 0; i < per_thread; ++i) {
+      int lo;
+      const int m = group_rows(a, e0 + i, &lo), n = (m + BM - 1) / BM * NT;
+      if (local < n) {
+        s_hit[0] = e0 + i;
+        s_hit[1] = lo;
+        s_hit[2] = m;
+        s_hit[3] = local;
+        break;
+      }
+      local -= n;
     }
-    const int first = before + incl - tiles * NT;
-    if (item >= first && item < before + incl) {
-      s_hit[0] = c0 + tid;
-      s_hit[1] = lo;
-      s_hit[2] = m;
-      s_hit[3] = item - first;
-    }
-    __syncthreads();
-    if (item < base) break;
   }
+  __syncthreads();
   it->e = __builtin_amdgcn_readfirstlane(s_hit[0]);
   it->lo = __builtin_amdgcn_readfirstlane(s_hit[1]);
   const int m = __builtin_amdgcn_readfirstlane(s_hit[2]), local = __builtin_amdgcn_readfirstlane(s_hit[3]);
@@ -214,6 +208,18 @@ __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
 
+__device__ __forceinline__ f32x4 fp8_mfma(u32x4 wl, u32x4 wh, u32x4 al, u32x4 ah) {
+  const i32x8 w = __builtin_bit_cast(i32x8, __builtin_shufflevector(wl, wh, 0, 1, 2, 3, 4, 5, 6, 7));
+  const i32x8 x = __builtin_bit_cast(i32x8, __builtin_shufflevector(al, ah, 0, 1, 2, 3, 4, 5, 6, 7));
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// 16 codes of either operand per lane: 64 products, as bf16
+__device__ __forceinline__ f32x4 fp8x_mfma(u32x4 w, u32x4 x, f32x4 p) {
+  p = mfma16(fp8x8_to_bf16x8(w[0], w[1]), fp8x8_to_bf16x8(x[0], x[1]), p);
+  return mfma16(fp8x8_to_bf16x8(w[2], w[3]), fp8x8_to_bf16x8(x[2], x[3]), p);
+}
+
 template <int TY, int EP, int WM, int WN, int MT, int NT, int STAGES>
 struct GroupTile {
   static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
@@ -224,7 +230,7 @@ struct GroupTile {
   static constexpr int NCOL = EP == GE_GLU ? BN / 2 : BN;  // outputs per row of a tile
   static constexpr int STAGE_BYTES = (BM + BN) * kStepBytes + (FP8 ? WAVES * 256 : 0);
   static_assert(AL >= 1 && WL >= 1 && AL * WAVES * 8 == BM && WL * WAVES * 8 == BN, "whole direct loads");
-  static_assert(NT % 2 == 0 && (EP != GE_GLU || (NT == 4 && WL * 8 <= 32 && 32 % (WL * 8) == 0)), "tile pairs");
+  static_assert(NT % 2 == 0 && (EP != GE_GLU || NT == 4), "tile pairs");
   static_assert(BM / WAVES <= 64, "one row scale per lane");
 
 
@@ -266,8 +272,8 @@ struct GroupTile {
     };
     const uint8_t *abase = a.A + a_first * a.lda;
     const uint32_t abytes = uint32_t((a_count - 1) * a.lda + a.Kb);
-    const bool up = EP == GE_GLU && ((wave * WL * 8) % (NT * 16)) >= 32;
-    const uint8_t *wbase = blob + (up ? a.off_w1 : a.off_w0) + uint64_t(n0) * uint64_t(a.ldw);
+    const uint8_t *wbase = blob + a.off_w0 + uint64_t(n0) * uint64_t(a.ldw);
+    const uint64_t to_up = EP == GE_GLU ? a.off_w1 - a.off_w0 : 0;  // GLU: from gate's rows to up's
     const uint32_t wbytes = uint32_t((min(NCOL, a.N - n0) - 1) * a.ldw + a.Kb);
     uint32_t aoff[AL], woff[WL];
 #pragma unroll
@@ -313,7 +319,7 @@ struct GroupTile {
     // nothing (empty buffers, so that every step has the same instructions in
     // flight).
     struct Loads {
-      u32x4 ares, wres, sres;
+      u32x4 ares, wres[EP == GE_GLU ? 2 : 1], sres;
       uint32_t at, st, ss;
     };
     auto plan = [&](int c, uint32_t at) FT_INLINE {
@@ -325,13 +331,15 @@ struct GroupTile {
       l.st = live ? uint32_t(ks) * kStepBytes : 0u;
       l.ss = live ? uint32_t(ks) * 4u : 0u;
       l.ares = rsrc_words(abase, live ? abytes : 0u);
-      l.wres = rsrc_words(wbase, live ? wbytes : 0u);
+      l.wres[0] = rsrc_words(wbase, live ? wbytes : 0u);
+      if constexpr (EP == GE_GLU) l.wres[1] = rsrc_words(wbase + to_up, live ? wbytes : 0u);
       if constexpr (FP8) l.sres = rsrc_words(sbase, live ? uint32_t(a_count * a.KB * 4) : 0u);
       return l;
     };
     auto load = [&](const Loads &l, int t) FT_INLINE {  // the t-th of them, 0 .. LOADS - 1
+      const bool up = EP == GE_GLU && ((wave * WL + t) * 8) % (NT * 16) >= 32;
       if (t < WL)
-        lds_load16(l.wres, l.at + BM * kStepBytes + (wave * WL + t) * 1024, woff[t], l.st);
+        lds_load16(up ? l.wres[EP == GE_GLU] : l.wres[0], l.at + BM * kStepBytes + (wave * WL + t) * 1024, woff[t], l.st);
       else if (t < WL + AL)
         lds_load16(l.ares, l.at + (wave * AL + t - WL) * 1024, aoff[t - WL], l.st);
       else
@@ -484,18 +492,6 @@ struct GroupTile {
         }
       }
     }
-  }
-
-  static __device__ __forceinline__ f32x4 fp8_mfma(u32x4 wl, u32x4 wh, u32x4 al, u32x4 ah) {
-    const i32x8 w = __builtin_bit_cast(i32x8, __builtin_shufflevector(wl, wh, 0, 1, 2, 3, 4, 5, 6, 7));
-    const i32x8 x = __builtin_bit_cast(i32x8, __builtin_shufflevector(al, ah, 0, 1, 2, 3, 4, 5, 6, 7));
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-  }
-
-  // 16 codes of either operand per lane: 64 products, as bf16
-  static __device__ __forceinline__ f32x4 fp8x_mfma(u32x4 w, u32x4 x, f32x4 p) {
-    p = mfma16(fp8x8_to_bf16x8(w[0], w[1]), fp8x8_to_bf16x8(x[0], x[1]), p);
-    return mfma16(fp8x8_to_bf16x8(w[2], w[3]), fp8x8_to_bf16x8(x[2], x[3]), p);
   }
 
   // Eight consecutive outputs n .. n+7 of a row, those below N.
