@@ -1,7 +1,6 @@
 // ft_fp8_gemm, ft_grouped_gemm and the FP8 experts of ft_moe_grouped_ffn: the
 // entry points and launches of the products in group_gemm.hpp.
 #include <algorithm>
-#include <cstdlib>
 
 #include "ft_internal.hpp"
 #include "group_gemm.hpp"
@@ -85,8 +84,7 @@ static bool stream_covers(const GroupArgs &a) {
 // bf16: 136 us against 156).
 static bool stream_choice(const GroupArgs &a, int64_t cols) {
   if (a.rows > (a.offsets != nullptr ? 16 * std::min(a.E, a.rows) : 128)) return false;
-  static const char *e = getenv("FTMOE_ST");
-  return row_tiles(a, 32) * cdiv<int64_t>(cols, 64) < (e ? atoi(e) : 192) && stream_covers(a);
+  return row_tiles(a, 32) * cdiv<int64_t>(cols, 64) < 200 && stream_covers(a);
 }
 
 template <int TY, int EP, int GX>
@@ -119,10 +117,16 @@ static int tile_choice(const GroupArgs &a, int cols256) {
 
 template <int TY, int EP>
 static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
-  constexpr bool GLU = EP == GE_GLU;
-  switch (tile_choice(a, GLU ? 128 : 256)) {
+  constexpr bool GLU = is_glu(EP);
+  const int tile = tile_choice(a, GLU ? 128 : 256);
+  switch (tile) {
     case TILE_256: return launch_tiles<TY, EP, 2, 4, 8, 4, 2>(a, stream);
     case TILE_128: return launch_tiles<TY, EP, 2, 4, 4, 4, 3>(a, stream);
+    default: break;
+  }
+  // (quantized hidden rows come from tiles of whole blocks only)
+  if constexpr (EP == GE_GLUQ) return fail(FT_ENOTSUP, "grouped product: no tile of whole blocks");
+  else switch (tile) {
     case TILE_64: return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
     default: return launch_tiles<TY, EP, 2, 2, 1, GLU ? 4 : 2, GLU ? 3 : 4>(a, stream);
   }
@@ -170,6 +174,7 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
   const int H = L.H, I = L.I, routed = f.T * f.k, rows = routed + (f.shared_blob != nullptr ? f.T : 0);
   const Fp8FfnWorkspace W = fp8_ffn_workspace(f.T, f.k, H, I);
   uint8_t *ws = static_cast<uint8_t *>(f.workspace);
+  float *xs = reinterpret_cast<float *>(ws + W.xs), *hs = reinterpret_cast<float *>(ws + W.hs);
   GroupArgs a{};
   a.pool = static_cast<const uint8_t *>(f.slot_pool);
   a.expert_bytes = L.expert_bytes;
@@ -181,51 +186,68 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
   a.rows = routed;
   a.T = f.T;
   a.k = f.k;
+  GroupArgs g = a;  // gate and up
+  g.off_w0 = L.off_gate;
+  g.off_w1 = L.off_up;
+  g.off_s0 = L.off_sgate;
+  g.off_s1 = L.off_sup;
+  g.ldw = g.Kb = H;
+  g.KB = cdiv(H, kFp8Block);
+  g.N = I;
+  g.sorted_rows = f.sorted_rows;
+  g.a_rows = f.T;
+  g.out = ws + W.h;
+  g.ldo = I;
+  GroupArgs d = a;  // down
+  d.off_w0 = d.off_w1 = L.off_down;
+  d.off_s0 = d.off_s1 = L.off_sdown;
+  d.ldw = d.Kb = I;
+  d.KB = cdiv(I, kFp8Block);
+  d.N = H;
+  d.a_rows = rows;
+  d.a_shared0 = routed;
+  d.out = f.y_rows;
+  d.ldo = H;
+  d.out_shared = f.y_shared;
+  // Three ways, the same for both stages whatever the call runs of them:
+  //  - few rows and tiles: the stream kernels quantize x and the hidden rows as
+  //    they read them (bf16 and fp32), two launches in all (1 token, 2 of 16
+  //    experts, H 2048, I 768: 15 against 22 us);
+  //  - tiles of whole 128-blocks of the hidden rows quantize them as they write
+  //    them (4096 tokens of 256 experts, H 4096, I 2048: 1.69 against 1.77 ms);
+  //  - smaller tiles leave them in fp32, quantized by a launch of their own.
+  a.N = std::max(H, I);
+  if (stream_choice(a, 2 * int64_t(I))) {
+    g.A = static_cast<const uint8_t *>(f.x);
+    g.lda = 2 * int64_t(H);
+    d.A = ws + W.h;
+    d.lda = 4 * int64_t(I);
+    ft_status st = FT_OK;
+    if (f.gate_up) st = launch_stream<GT_FP8, GE_GLU, GX_BF16>(g, stream);
+    if (st == FT_OK && f.down) st = launch_stream<GT_FP8, GE_F32, GX_F32>(d, stream);
+    return st;
+  }
+  g.A = ws + W.xq;
+  g.lda = H;
+  g.As = xs;
+  d.A = ws + W.hq;
+  d.lda = I;
+  d.As = hs;
   ft_status st = FT_OK;
-  a.N = std::max(H, I);  // (of the larger stage, for the choice)
-  const bool stream_it = stream_choice(a, 2 * int64_t(I));
   if (f.gate_up) {
-    if (!stream_it) st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, reinterpret_cast<float *>(ws + W.xs), stream);
-    if (!stream_it && st != FT_OK) return st;
-    GroupArgs g = a;
-    g.A = stream_it ? static_cast<const uint8_t *>(f.x) : ws + W.xq;
-    g.lda = stream_it ? 2 * H : H;
-    g.As = reinterpret_cast<const float *>(ws + W.xs);
-    g.off_w0 = L.off_gate;
-    g.off_w1 = L.off_up;
-    g.off_s0 = L.off_sgate;
-    g.off_s1 = L.off_sup;
-    g.ldw = g.Kb = H;
-    g.KB = cdiv(H, kFp8Block);
-    g.N = I;
-    g.sorted_rows = f.sorted_rows;
-    g.a_rows = f.T;
-    g.out = ws + W.h;
-    g.ldo = I;
-    st = stream_it ? launch_stream<GT_FP8, GE_GLU, GX_BF16>(g, stream) : launch_products<GT_FP8, GE_GLU>(g, stream);
+    st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, xs, stream);
+    if (st != FT_OK) return st;
+    if (tile_choice(g, 128) >= TILE_128) {
+      g.out = ws + W.hq;
+      g.out_scales = hs;
+      st = launch_products<GT_FP8, GE_GLUQ>(g, stream);
+    } else {
+      st = launch_products<GT_FP8, GE_GLU>(g, stream);
+      if (st == FT_OK) st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, hs, stream);
+    }
     if (st != FT_OK) return st;
   }
-  if (f.down) {
-    if (!stream_it) st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, reinterpret_cast<float *>(ws + W.hs), stream);
-    if (!stream_it && st != FT_OK) return st;
-    GroupArgs d = a;
-    d.A = stream_it ? ws + W.h : ws + W.hq;
-    d.lda = stream_it ? 4 * int64_t(I) : I;
-    d.As = reinterpret_cast<const float *>(ws + W.hs);
-    d.off_w0 = d.off_w1 = L.off_down;
-    d.off_s0 = d.off_s1 = L.off_sdown;
-    d.ldw = d.Kb = I;
-    d.KB = cdiv(I, kFp8Block);
-    d.N = H;
-    d.a_rows = rows;
-    d.a_shared0 = routed;
-    d.out = f.y_rows;
-    d.ldo = H;
-    d.out_shared = f.y_shared;
-    st = stream_it ? launch_stream<GT_FP8, GE_F32, GX_F32>(d, stream) : launch_products<GT_FP8, GE_F32>(d, stream);
-    if (st != FT_OK) return st;
-  }
-  return FT_OK;
+  return f.down ? launch_products<GT_FP8, GE_F32>(d, stream) : FT_OK;
 }
 
 }  // namespace ft

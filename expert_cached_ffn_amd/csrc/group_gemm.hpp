@@ -16,9 +16,8 @@
 //
 // The weights are the MFMA's A operand and the rows its B operand, so a lane
 // (r, q) of a 16 x 16 accumulator holds row r's outputs of weight rows
-// 4q .. 4q+3.  The weight rows of a pair of tiles are laid out in LDS such
-// that a lane's two accumulators are 8 consecutive outputs (one 16-byte bf16
-// store), and a row's scale is one value per lane.
+// 4q .. 4q+3 (16 bytes of fp32; bf16: see col_of), and a row's scale is one
+// value per lane.
 //
 // Rows of the tile past the group's end, weight rows past N and chunks past K
 // are loaded with an out-of-range offset: zeros, no memory traffic.
@@ -43,7 +42,9 @@
 namespace ft {
 
 enum { GT_BF16 = 0, GT_FP8 = 1, GT_FP8X = 2 };  // operand type / instruction
-enum { GE_F32 = 0, GE_BF16 = 1, GE_GLU = 2 };   // outputs: the products in fp32 or bf16; silu(gate) * up in fp32
+// outputs: the products in fp32 or bf16; silu(gate) * up in fp32, or quantized by 1 x 128 blocks
+enum { GE_F32 = 0, GE_BF16 = 1, GE_GLU = 2, GE_GLUQ = 3 };
+constexpr bool is_glu(int ep) { return ep == GE_GLU || ep == GE_GLUQ; }
 
 // lambdas that hold register arrays: a call would put those into memory
 #define FT_INLINE __attribute__((always_inline))
@@ -72,6 +73,7 @@ struct GroupArgs {
   int a_shared0;                  // first A row of the shared group
   void *out;
   int64_t ldo;                    // elements
+  float *out_scales;              // GE_GLUQ: scales of the rows in out, [rows, ceil(N / 128)]
   float *out_shared;              // rows of the shared group (NULL: behind the others in out)
   int n_ntiles;
 };
@@ -226,11 +228,12 @@ struct GroupTile {
   static constexpr int BM = WM * MT * 16, BN = WN * NT * 16;
   static constexpr int AL = BM / 8 / WAVES, WL = BN / 8 / WAVES;  // direct loads per wave and step
   static constexpr bool FP8 = TY != GT_BF16;
+  static constexpr bool GLU = is_glu(EP);
   static constexpr int LOADS = AL + WL + (FP8 ? 1 : 0);
-  static constexpr int NCOL = EP == GE_GLU ? BN / 2 : BN;  // outputs per row of a tile
+  static constexpr int NCOL = GLU ? BN / 2 : BN;  // outputs per row of a tile
   static constexpr int STAGE_BYTES = (BM + BN) * kStepBytes + (FP8 ? WAVES * 256 : 0);
   static_assert(AL >= 1 && WL >= 1 && AL * WAVES * 8 == BM && WL * WAVES * 8 == BN, "whole direct loads");
-  static_assert(NT % 2 == 0 && (EP != GE_GLU || NT == 4), "tile pairs");
+  static_assert(NT % 2 == 0 && (!GLU || NT == 4), "tile pairs");
   static_assert(BM / WAVES <= 64, "one row scale per lane");
 
 
@@ -241,12 +244,14 @@ struct GroupTile {
     return n < LOADS ? n : LOADS;
   }
 
-  // Output of weight row p of the tile's LDS order, relative to the tile's first:
-  // pairs of 16-row tiles are interleaved by 4 so that a lane's two
-  // accumulators are consecutive.
+  // Output of weight row p of the tile's LDS order, relative to the tile's first.
+  // fp32: as they come, 4 outputs (16 bytes) per lane and 64 bytes per row and
+  // store.  bf16 and codes: pairs of 16-row tiles interleaved by 4, so that a
+  // lane's two accumulators are 8 consecutive outputs.
   static __device__ __forceinline__ int col_of(int p) {
-    const int pl = p % (NT * 16), f = 8 * ((pl & 15) >> 2) + 4 * ((pl >> 4) & 1) + (pl & 3);
-    if (EP == GE_GLU) return p / (NT * 16) * 32 + f;
+    const int pl = p % (NT * 16);
+    const int f = EP == GE_F32 || EP == GE_GLU ? pl & 31 : 8 * ((pl & 15) >> 2) + 4 * ((pl >> 4) & 1) + (pl & 3);
+    if (GLU) return p / (NT * 16) * 32 + f;
     return p / (NT * 16) * (NT * 16) + (pl & ~31) + f;
   }
 
@@ -273,7 +278,7 @@ struct GroupTile {
     const uint8_t *abase = a.A + a_first * a.lda;
     const uint32_t abytes = uint32_t((a_count - 1) * a.lda + a.Kb);
     const uint8_t *wbase = blob + a.off_w0 + uint64_t(n0) * uint64_t(a.ldw);
-    const uint64_t to_up = EP == GE_GLU ? a.off_w1 - a.off_w0 : 0;  // GLU: from gate's rows to up's
+    const uint64_t to_up = GLU ? a.off_w1 - a.off_w0 : 0;  // GLU: from gate's rows to up's
     const uint32_t wbytes = uint32_t((min(NCOL, a.N - n0) - 1) * a.ldw + a.Kb);
     uint32_t aoff[AL], woff[WL];
 #pragma unroll
@@ -304,42 +309,36 @@ struct GroupTile {
     if constexpr (FP8) {
       const int src = lane < BM / WAVES ? a_row(wave * (BM / WAVES) + lane) : -1;
       if (src >= 0) soff = uint32_t(src) * uint32_t(a.KB) * 4u;
-      const int nb = min((n0 + wn * (EP == GE_GLU ? 32 : NT * 16)) / 128, cdiv(a.N, 128) - 1);
+      const int nb = min((n0 + wn * (GLU ? 32 : NT * 16)) / 128, cdiv(a.N, 128) - 1);
       swp0 = reinterpret_cast<const float *>(blob + a.off_s0) + int64_t(nb) * a.KB;
-      if (EP == GE_GLU) swp1 = reinterpret_cast<const float *>(blob + a.off_s1) + int64_t(nb) * a.KB;
+      if (GLU) swp1 = reinterpret_cast<const float *>(blob + a.off_s1) + int64_t(nb) * a.KB;
     }
-    // Tiles start at different steps (within 2 KB of each other's columns) and
-    // wrap around: side by side on one XCD, they would all ask the same L2
-    // channels at once (dense 8192 x 4096 x 4096: 137 -> 134 us).
-    const int first = tail == 0 ? (it.nt + it.row0 / BM + it.e) % min(16, nk) : 0;
-    auto step_of = [&](int c) { return c + first < nk ? c + first : c + first - nk; };
     const float *sbase = FP8 ? a.As + a_first * a.KB : nullptr;
     const uint32_t ldsb = __builtin_amdgcn_readfirstlane(lds_address(L));
     // Step c's loads, into the ring at byte `at`.  A step past the end loads
     // nothing (empty buffers, so that every step has the same instructions in
     // flight).
     struct Loads {
-      u32x4 ares, wres[EP == GE_GLU ? 2 : 1], sres;
+      u32x4 ares, wres[GLU ? 2 : 1], sres;
       uint32_t at, st, ss;
     };
     auto plan = [&](int c, uint32_t at) FT_INLINE {
       const bool live = c < nk;
       if (tail != 0 && c == nk - 1) cut();
-      const int ks = step_of(c);
       Loads l;
       l.at = ldsb + at;
-      l.st = live ? uint32_t(ks) * kStepBytes : 0u;
-      l.ss = live ? uint32_t(ks) * 4u : 0u;
+      l.st = live ? uint32_t(c) * kStepBytes : 0u;
+      l.ss = live ? uint32_t(c) * 4u : 0u;
       l.ares = rsrc_words(abase, live ? abytes : 0u);
       l.wres[0] = rsrc_words(wbase, live ? wbytes : 0u);
-      if constexpr (EP == GE_GLU) l.wres[1] = rsrc_words(wbase + to_up, live ? wbytes : 0u);
+      if constexpr (GLU) l.wres[1] = rsrc_words(wbase + to_up, live ? wbytes : 0u);
       if constexpr (FP8) l.sres = rsrc_words(sbase, live ? uint32_t(a_count * a.KB * 4) : 0u);
       return l;
     };
     auto load = [&](const Loads &l, int t) FT_INLINE {  // the t-th of them, 0 .. LOADS - 1
-      const bool up = EP == GE_GLU && ((wave * WL + t) * 8) % (NT * 16) >= 32;
+      const bool up = GLU && ((wave * WL + t) * 8) % (NT * 16) >= 32;
       if (t < WL)
-        lds_load16(up ? l.wres[EP == GE_GLU] : l.wres[0], l.at + BM * kStepBytes + (wave * WL + t) * 1024, woff[t], l.st);
+        lds_load16(up ? l.wres[GLU] : l.wres[0], l.at + BM * kStepBytes + (wave * WL + t) * 1024, woff[t], l.st);
       else if (t < WL + AL)
         lds_load16(l.ares, l.at + (wave * AL + t - WL) * 1024, aoff[t - WL], l.st);
       else
@@ -360,9 +359,9 @@ struct GroupTile {
     int sw_first = 0;
     auto load_weight_scales = [&](int c) {
       sw_first = c;
-      const int b = step_of(min(c + lane, nk - 1));
+      const int b = min(c + lane, a.KB - 1);
       swv0 = swp0[b];
-      if (EP == GE_GLU) swv1 = swp1[b];
+      if (GLU) swv1 = swp1[b];
     };
 
     // ---- operands of one step: the weights' in registers for the whole step, the
@@ -399,7 +398,7 @@ struct GroupTile {
       float sw0 = 0.f, sw1 = 0.f;
       if constexpr (FP8) {
         sw0 = lane_value(swv0, c - sw_first);
-        if (EP == GE_GLU) sw1 = lane_value(swv1, c - sw_first);
+        if (GLU) sw1 = lane_value(swv1, c - sw_first);
       }
       read_a(0, buf);
       read_w(buf);
@@ -422,10 +421,10 @@ struct GroupTile {
           }
         }
         if constexpr (FP8) {
-          const float s0 = f.sa[i & 1] * sw0, s1 = EP == GE_GLU ? f.sa[i & 1] * sw1 : s0;
+          const float s0 = f.sa[i & 1] * sw0, s1 = GLU ? f.sa[i & 1] * sw1 : s0;
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const float s = EP == GE_GLU && j >= NT / 2 ? s1 : s0;
+            const float s = GLU && j >= NT / 2 ? s1 : s0;
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[j][v], s, acc[i][j][v]);
           }
@@ -464,45 +463,77 @@ struct GroupTile {
     wait_vmcnt<0>();
 
     // ---- epilogue
+    const int64_t orow0 = int64_t(shared ? a.rows : it.lo) + it.row0;
+    if constexpr (EP == GE_GLUQ) {
+      // A tile holds whole 128-blocks of its hidden rows, 32 columns in each of 4
+      // waves: their largest magnitudes meet in LDS.  silu(gate) * up goes back
+      // into gate's registers meanwhile.
+      static_assert(NCOL == 128 && WN == 4, "one block per row and tile");
+      __shared__ uint32_t s_max[4][BM];
 #pragma unroll
-    for (int i = 0; i < MTR; ++i) {
-      const int rr = (i * WM + wm) * 16 + r;
-      if (rr >= it.m) continue;
-      if constexpr (EP == GE_GLU) {
-        float *o = static_cast<float *>(a.out) + (int64_t(shared ? a.rows : it.lo) + it.row0 + rr) * a.ldo;
-        const int n = n0 + wn * 32 + 8 * q;
-        float v[8];
+      for (int i = 0; i < MTR; ++i) {
+        uint32_t m = 0;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float g = acc[i][u / 4][u % 4];
-          v[u] = silu(g) * acc[i][2 + u / 4][u % 4];
+          float &g = reinterpret_cast<float *>(&acc[i][u / 4])[u % 4];
+          g = silu(g) * acc[i][2 + u / 4][u % 4];
+          m = max(m, __float_as_uint(g) & 0x7fffffffu);
         }
-        store8(o, n, a.N, v, a.ldo % 4 == 0);
-      } else {
-        using O = std::conditional_t<EP == GE_BF16, uint16_t, float>;
-        const bool own = EP == GE_F32 && shared && a.out_shared != nullptr;
-        O *o = own ? reinterpret_cast<O *>(a.out_shared) + int64_t(it.row0 + rr) * a.ldo
-                   : static_cast<O *>(a.out) + (int64_t(shared ? a.rows : it.lo) + it.row0 + rr) * a.ldo;
+        m = max(m, uint32_t(__shfl_xor(int(m), 16)));
+        m = max(m, uint32_t(__shfl_xor(int(m), 32)));
+        if (q == 0) s_max[wn][(i * WM + wm) * 16 + r] = m;
+      }
+      __syncthreads();
 #pragma unroll
-        for (int jj = 0; jj < NT / 2; ++jj) {
-          float v[8];
+      for (int i = 0; i < MTR; ++i) {
+        const int rr = (i * WM + wm) * 16 + r, n = n0 + wn * 32 + 8 * q;
+        if (rr >= it.m) continue;
+        const Fp8Scale sc = fp8_scale(max(max(s_max[0][rr], s_max[1][rr]), max(s_max[2][rr], s_max[3][rr])));
+        float v[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = acc[i][2 * jj + u / 4][u % 4];
-          store8(o, n0 + wn * NT * 16 + 32 * jj + 8 * q, a.N, v, a.ldo % (16 / sizeof(O)) == 0);
+        for (int u = 0; u < 8; ++u) v[u] = acc[i][u / 4][u % 4];
+        if (n < a.N) *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.out) + (orow0 + rr) * a.ldo + n) = fp8_codes8(v, sc.inv);
+        if (wn == 0 && q == 0) a.out_scales[(orow0 + rr) * cdiv(a.N, 128) + it.nt] = sc.scale;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MTR; ++i) {
+        const int rr = (i * WM + wm) * 16 + r;
+        if (rr >= it.m) continue;
+        if constexpr (EP == GE_BF16) {
+          uint16_t *o = static_cast<uint16_t *>(a.out) + (orow0 + rr) * a.ldo;
+#pragma unroll
+          for (int jj = 0; jj < NT / 2; ++jj) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = acc[i][2 * jj + u / 4][u % 4];
+            store8(o, n0 + wn * NT * 16 + 32 * jj + 8 * q, a.N, v, a.ldo % 8 == 0);
+          }
+        } else {
+          const bool own = !GLU && shared && a.out_shared != nullptr;
+          float *o = own ? a.out_shared + int64_t(it.row0 + rr) * a.ldo : static_cast<float *>(a.out) + (orow0 + rr) * a.ldo;
+#pragma unroll
+          for (int j = 0; j < (GLU ? NT / 2 : NT); ++j) {
+            f32x4 v = acc[i][j];
+            if constexpr (GLU) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) v[u] = silu(v[u]) * acc[i][2 + j][u];
+            }
+            store4(o, n0 + wn * (GLU ? 32 : NT * 16) + 16 * j + 4 * q, a.N, v, a.ldo % 4 == 0);
+          }
         }
       }
     }
   }
 
-  // Eight consecutive outputs n .. n+7 of a row, those below N.
-  static __device__ __forceinline__ void store8(float *o, int n, int N, const float (&v)[8], bool vec) {
-    if (vec && n + 8 <= N) {
-      *reinterpret_cast<f32x4 *>(o + n) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4 *>(o + n + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  // Four (eight) consecutive outputs from n on, those below N.
+  static __device__ __forceinline__ void store4(float *o, int n, int N, f32x4 v, bool vec) {
+    if (vec && n + 4 <= N) {
+      *reinterpret_cast<f32x4 *>(o + n) = v;
       return;
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < 4; ++u)
       if (n + u < N) o[n + u] = v[u];
   }
   static __device__ __forceinline__ void store8(uint16_t *o, int n, int N, const float (&v)[8], bool vec) {
@@ -522,6 +553,7 @@ struct GroupTile {
   // The rows of a group whose weights are not resident.
   static __device__ __forceinline__ void fill_nan(const GroupArgs &a, const GroupItem &it) {
     const int n0 = it.nt * NCOL, w = min(NCOL, a.N - n0);
+    if constexpr (EP == GE_GLUQ) return;  // the next stage writes their NaN without reading these
     for (int u = threadIdx.x; u < it.m * w; u += THREADS) {
       const int64_t at = (int64_t(it.lo) + it.row0 + u / w) * a.ldo + n0 + u % w;
       if (EP == GE_BF16)
