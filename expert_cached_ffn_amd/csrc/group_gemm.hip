@@ -55,9 +55,10 @@ static int resident(K kernel, int threads) {
       hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0)
     cus = 256;
   if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, reinterpret_cast<const void *>(kernel), threads, 0) != hipSuccess ||
-      per <= 0)
+      per <= 0) {
+    (void)hipGetLastError();
     per = 1;
-  (void)hipGetLastError();
+  }
   return cus * per;
 }
 
@@ -73,7 +74,7 @@ static ft_status launch_stream_as(GroupArgs a, hipStream_t stream) {
 }
 
 static bool stream_covers(const GroupArgs &a) {
-  return a.E <= kStreamMaxE && a.rows <= kStreamMaxRows && (a.shared_blob == nullptr || a.T <= 256) &&
+  return a.E <= kStreamMaxE && a.rows <= kStreamMaxRows && (a.shared_blob == nullptr || a.T <= kStreamMaxT) &&
          int64_t(row_sets(a)) * cdiv(a.N, 16) < (int64_t(1) << 30);
 }
 
@@ -82,7 +83,7 @@ static bool stream_covers(const GroupArgs &a) {
 // us; 77 rows by 1001 x 2000 in fp32: 7.5 against 10.2).  With enough tiles the
 // LDS ring keeps more of the weights on their way (64 tokens, 128 experts,
 // bf16: 136 us against 156).
-static bool stream_choice(const GroupArgs &a, int64_t cols) {
+static bool stream_choice(const GroupArgs &a, int64_t cols) {  // cols: weight rows per group
   if (a.rows > (a.offsets != nullptr ? 16 * std::min(a.E, a.rows) : 128)) return false;
   return row_tiles(a, 32) * cdiv<int64_t>(cols, 64) < 200 && stream_covers(a);
 }

@@ -131,6 +131,7 @@ __device__ __forceinline__ bool group_item(const GroupArgs &a, GroupItem *it) {
   }
   const int incl = wave_incl_scan_i32(mine);
   if (lane == 63) s_cnt[wave] = incl;
+  if (tid == 0) s_hit[0] = -1;  // offsets that are no offsets may leave an item without a group
   __syncthreads();
   int total = 0, first = incl - mine;
 #pragma unroll
@@ -171,6 +172,7 @@ __device__ __forceinline__ bool group_item(const GroupArgs &a, GroupItem *it) {
   }
   __syncthreads();
   it->e = __builtin_amdgcn_readfirstlane(s_hit[0]);
+  if (it->e < 0) return false;
   it->lo = __builtin_amdgcn_readfirstlane(s_hit[1]);
   const int m = __builtin_amdgcn_readfirstlane(s_hit[2]), local = __builtin_amdgcn_readfirstlane(s_hit[3]);
   const int tiles = (m + BM - 1) / BM;

@@ -30,8 +30,9 @@ namespace ft {
 enum { GX_SAME = 0, GX_BF16 = 1, GX_F32 = 2 };  // row operand: as the weights (FP8: codes and scales); to be quantized
 
 constexpr int kStreamMaxE = 1024;     // groups of the LDS table (and one shared)
-constexpr int kStreamMaxRows = 4096;  // rows: at most kStreamMaxSets row sets
-constexpr int kStreamMaxSets = kStreamMaxE + 1 + kStreamMaxRows / 16;
+constexpr int kStreamMaxRows = 4096;
+constexpr int kStreamMaxT = 256;      // rows of the shared group
+constexpr int kStreamMaxSets = kStreamMaxE + kStreamMaxRows / 16 + kStreamMaxT / 16;  // row sets of all groups, at most
 
 template <int TY, int EP, int GX, int WAVES, int BPW>
 struct GroupStream {

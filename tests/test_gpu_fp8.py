@@ -292,9 +292,10 @@ def test_grouped_slots_and_short_offsets(ops, dtype, T, k, E):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP8])
-def test_grouped_many_groups(ops, dtype):
-    """4096 groups, the limit, most of them empty or of one row; then all rows in the last one."""
-    T, k, E, N, K = 300, 2, 4096, 16, 32
+@pytest.mark.parametrize("E", [64, 1024, 4096])
+def test_grouped_many_groups(ops, dtype, E):
+    """Up to 4096 groups, the limit, many of them empty or of one row; then all rows in the last one."""
+    T, k, N, K = 300, 2, 16, 32
     rng = np.random.default_rng(3)
     counts = rng.multinomial(T * k, np.full(E, 1 / E))
     d = make_grouped(gen(4), rng, dtype, T, k, E, N, K, True, counts)
@@ -309,6 +310,33 @@ def test_grouped_many_groups(ops, dtype):
     last[E] = T * k
     o = run_grouped(ops, d, dtype, T, k, E, N, K, F32, off=last)
     check_product(o, a, d["w64"][E - 1], K, F32, False, "last")
+
+
+def test_rows_past_four_gigabytes(ops):
+    """Operand rows whose byte offsets pass 32 bits, dense and in groups; the rows at the far end are checked."""
+    M, N, K = 1_060_000, 32, 4096
+    g = gen(21)
+    base = codes_of(g, 5000, K)
+    a = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    for i in range(0, M, 5000):
+        a[i:i + 5000] = base[:min(5000, M - i)].roll(i // 5000, 0)
+    assert a.numel() > 1 << 32
+    sa, w, sw = scales_of(g, M, 32), codes_of(g, 2, N, K), scales_of(g, 2, 1, 32)
+    o = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    ops.ft_fp8_gemm(a, K, sa, w[0], K, sw[0], M, N, K, BF16, o, N)
+    torch.cuda.synchronize()
+    for at in (0, 524_000, 1_048_500, M - 300):
+        check_product(o[at:at + 300], values(a[at:at + 300], sa[at:at + 300], 1), values(w[0], sw[0], 128), K, BF16, True, at)
+    stride = N * K + 256
+    pool = torch.zeros((2, stride), dtype=torch.uint8, device="cuda")
+    for e in range(2):
+        pool[e, :N * K] = w[e].reshape(-1)
+        pool[e, N * K:N * K + 128] = sw[e].reshape(-1).view(torch.uint8)
+    off = torch.tensor([0, 1_048_700, M], dtype=torch.int32, device="cuda")
+    ops.ft_grouped_gemm(FP8, a, K, sa, pool, stride, 0, N * K, 2, None, M, 1, 2, off, None, N, K, BF16, o, N)
+    torch.cuda.synchronize()
+    for at, e in ((0, 0), (1_048_400, 0), (1_048_700, 1), (M - 300, 1)):
+        check_product(o[at:at + 300], values(a[at:at + 300], sa[at:at + 300], 1), values(w[e], sw[e], 128), K, BF16, True, at)
 
 
 def test_results_repeat_and_streams(ops):
