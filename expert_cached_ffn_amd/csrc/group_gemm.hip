@@ -116,21 +116,20 @@ static int tile_choice(const GroupArgs &a, int cols256) {
   return mean > 32 ? TILE_64 : TILE_32;
 }
 
+// fp8_ffn asks for GE_GLUQ where the tiles hold whole blocks, for GE_GLU elsewhere.
 template <int TY, int EP>
 static ft_status launch_products(const GroupArgs &a, hipStream_t stream) {
   constexpr bool GLU = is_glu(EP);
   const int tile = tile_choice(a, GLU ? 128 : 256);
-  switch (tile) {
-    case TILE_256: return launch_tiles<TY, EP, 2, 4, 8, 4, 2>(a, stream);
-    case TILE_128: return launch_tiles<TY, EP, 2, 4, 4, 4, 3>(a, stream);
-    default: break;
+  if constexpr (EP != GE_GLU) {
+    if (tile == TILE_256) return launch_tiles<TY, EP, 2, 4, 8, 4, 2>(a, stream);
+    if (tile == TILE_128) return launch_tiles<TY, EP, 2, 4, 4, 4, 3>(a, stream);
   }
-  // (quantized hidden rows come from tiles of whole blocks only)
-  if constexpr (EP == GE_GLUQ) return fail(FT_ENOTSUP, "grouped product: no tile of whole blocks");
-  else switch (tile) {
-    case TILE_64: return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
-    default: return launch_tiles<TY, EP, 2, 2, 1, GLU ? 4 : 2, GLU ? 3 : 4>(a, stream);
+  if constexpr (EP != GE_GLUQ) {
+    if (tile == TILE_64) return launch_tiles<TY, EP, 2, 2, 2, GLU ? 4 : 2, 3>(a, stream);
+    if (tile == TILE_32) return launch_tiles<TY, EP, 2, 2, 1, GLU ? 4 : 2, GLU ? 3 : 4>(a, stream);
   }
+  return fail(FT_ENOTSUP, "grouped product: no tile of this form");
 }
 
 static ft_status group_products(int dtype, int out_dtype, const GroupArgs &a, hipStream_t stream) {
@@ -210,45 +209,63 @@ ft_status fp8_ffn(const Fp8Ffn &f, hipStream_t stream) {
   d.out = f.y_rows;
   d.ldo = H;
   d.out_shared = f.y_shared;
-  // Three ways, the same for both stages whatever the call runs of them:
-  //  - few rows and tiles: the stream kernels quantize x and the hidden rows as
-  //    they read them (bf16 and fp32), two launches in all (1 token, 2 of 16
-  //    experts, H 2048, I 768: 15 against 22 us);
-  //  - tiles of whole 128-blocks of the hidden rows quantize them as they write
-  //    them (4096 tokens of 256 experts, H 4096, I 2048: 1.69 against 1.77 ms);
-  //  - smaller tiles leave them in fp32, quantized by a launch of their own.
+  // The same choices whatever stages the call runs (the down stage has to find
+  // the hidden rows in the form it takes):
+  //  - gate/up of few rows and tiles: the stream kernel, which quantizes x as it
+  //    reads it (1 token, 2 of 16 experts, H 2048, I 768: 15 against 22 us for
+  //    the whole FFN);
+  //  - otherwise x is quantized by a launch of its own.  Tiles of whole 128-blocks
+  //    of the hidden rows quantize those as they write them (4096 tokens of 256
+  //    experts, H 4096, I 2048: 1.69 against 1.77 ms); smaller tiles leave them in
+  //    fp32;
+  //  - fp32 hidden rows go to the stream kernel for down if gate/up took it, or if
+  //    the tiles have few steps to hide their start behind (33 tokens, 8 of 128
+  //    experts, I 768: 113 against 116 us); else they are quantized by a launch
+  //    of their own.
+  // Gate/up sums decide the hidden rows' codes, where an error of 1.5e-5 moves
+  // about one value in 5000 to its neighbour: a token in 30 is then off by up to
+  // 8e-3 instead of a bf16 output's 1.7e-3.  Where the weights' read bounds the
+  // call the sums are exact (bf16 instruction: 116 against 114 us at 33 tokens);
+  // the whole-block tiles of large batches use the FP8 instruction (1.71 against
+  // 2.00 ms at 4096 tokens; all tokens together 2.0e-3 off).
   a.N = std::max(H, I);
-  if (stream_choice(a, 2 * int64_t(I))) {
+  const bool stream_gu = stream_choice(a, 2 * int64_t(I));
+  const bool whole = !stream_gu && tile_choice(g, 128) >= TILE_128;
+  const bool stream_dn =
+      stream_gu || (!whole && I <= 1024 && a.rows <= 16 * std::min(a.E, a.rows) && stream_covers(a));
+  ft_status st = FT_OK;
+  if (f.gate_up && stream_gu) {
     g.A = static_cast<const uint8_t *>(f.x);
     g.lda = 2 * int64_t(H);
-    d.A = ws + W.h;
-    d.lda = 4 * int64_t(I);
-    ft_status st = FT_OK;
-    if (f.gate_up) st = launch_stream<GT_FP8, GE_GLU, GX_BF16>(g, stream);
-    if (st == FT_OK && f.down) st = launch_stream<GT_FP8, GE_F32, GX_F32>(d, stream);
-    return st;
-  }
-  g.A = ws + W.xq;
-  g.lda = H;
-  g.As = xs;
-  d.A = ws + W.hq;
-  d.lda = I;
-  d.As = hs;
-  ft_status st = FT_OK;
-  if (f.gate_up) {
+    st = launch_stream<GT_FP8X, GE_GLU, GX_BF16>(g, stream);
+  } else if (f.gate_up) {
     st = fp8_quantize_launch(f.x, FT_BF16, H, f.T, H, 1, ws + W.xq, H, xs, stream);
     if (st != FT_OK) return st;
-    if (tile_choice(g, 128) >= TILE_128) {
+    g.A = ws + W.xq;
+    g.lda = H;
+    g.As = xs;
+    if (whole) {
       g.out = ws + W.hq;
       g.out_scales = hs;
       st = launch_products<GT_FP8, GE_GLUQ>(g, stream);
     } else {
-      st = launch_products<GT_FP8, GE_GLU>(g, stream);
-      if (st == FT_OK) st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, hs, stream);
+      st = launch_products<GT_FP8X, GE_GLU>(g, stream);
     }
+  }
+  if (st != FT_OK || !f.down) return st;
+  if (stream_dn) {
+    d.A = ws + W.h;
+    d.lda = 4 * int64_t(I);
+    return launch_stream<GT_FP8, GE_F32, GX_F32>(d, stream);
+  }
+  if (!whole) {
+    st = fp8_quantize_launch(ws + W.h, FT_F32, I, rows, I, 1, ws + W.hq, I, hs, stream);
     if (st != FT_OK) return st;
   }
-  return f.down ? launch_products<GT_FP8, GE_F32>(d, stream) : FT_OK;
+  d.A = ws + W.hq;
+  d.lda = I;
+  d.As = hs;
+  return launch_products<GT_FP8, GE_F32>(d, stream);
 }
 
 }  // namespace ft

@@ -212,8 +212,11 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  *   Other values: FT_ENOTSUP.
  *   FT_FP8 weights take FT_FFN_EXACT, in which the activations join them in
  *   FP8: x and the fp32 hidden vector are quantized exactly as ft_fp8_quantize
- *   does with block_rows 1, and the products are those of ft_fp8_gemm with
- *   bf16 outputs (sums good to about 16 bits), y_rows being fp32.
+ *   does with block_rows 1; y_rows are fp32.  The down products, and gate/up of
+ *   batches of at least 24 rows per expert, take the FP8 matrix instruction
+ *   (sums good to about 16 bits: see ft_fp8_gemm), so a hidden value next to a
+ *   border of E4M3 may get the neighbouring code; other gate/up products are
+ *   summed in fp32.
  * mode, stage bits: FT_FFN_GATE_UP_ONLY runs only the gate/up + SwiGLU stage
  *   (y is not written); FT_FFN_DOWN_ONLY runs only the down projection from
  *   the hidden rows in `workspace` (left there by a FT_FFN_GATE_UP_ONLY call
