@@ -1,6 +1,7 @@
 // Error text, version, expert blob layout and workspace sizing.
-#include "ft_internal.hpp"
+#include <algorithm>
 
+#include "ft_internal.hpp"
 
 namespace ft {
 
@@ -87,6 +88,11 @@ extern "C" ft_status ft_expert_layout_init(int32_t wdtype, int32_t H, int32_t I,
   return FT_OK;
 }
 
+// (FT_FP8's FFN needs more than the others', and the call does not say which it is for)
+static size_t any_ffn_workspace(int32_t T, int32_t k, int32_t H, int32_t I) {
+  return std::max(ft::ffn_workspace_bytes(FT_BF16, T, k, H, I), ft::ffn_workspace_bytes(FT_FP8, T, k, H, I));
+}
+
 extern "C" size_t ft_workspace_bytes(int32_t which, int32_t T, int32_t k, int32_t E, int32_t H,
                                      int32_t I) {
   if (T < 0 || k < 0 || E < 0 || H < 0 || I < 0) return 0;
@@ -94,11 +100,11 @@ extern "C" size_t ft_workspace_bytes(int32_t which, int32_t T, int32_t k, int32_
     case FT_WS_PERMUTE:
       return ft::permute_workspace_bytes(T, k, E);
     case FT_WS_FFN:
-      return ft::ffn_workspace_bytes(T, k, E, H, I);
+      return any_ffn_workspace(T, k, H, I);
     case FT_WS_ROUTE_PERMUTE:
       return ft::permute_workspace_bytes(T, k, E);
     case FT_WS_LAYER: {  // the one-token kernel's wait words, then the permutation's counts or the FFN's rows
-      const size_t a = ft::permute_workspace_bytes(T, k, E), b = ft::ffn_workspace_bytes(T, k, E, H, I);
+      const size_t a = ft::permute_workspace_bytes(T, k, E), b = any_ffn_workspace(T, k, H, I);
       return ft::kLayerWaitBytes + (a > b ? a : b);
     }
     default:

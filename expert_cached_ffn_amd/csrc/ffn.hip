@@ -49,12 +49,12 @@ static MxWorkspace mx_workspace_layout(int64_t T, int64_t k, int64_t H, int64_t 
   return w;
 }
 
-size_t ffn_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I) {
-  (void)E;
+size_t ffn_workspace_bytes(int32_t wdtype, int32_t T, int32_t k, int32_t H, int32_t I) {
+  if (wdtype == FT_FP8) return fp8_ffn_workspace_bytes(T, k, H, I);
   const uint64_t rows = uint64_t(T) * uint64_t(k) + uint64_t(T);
   const uint64_t b = (rows * uint64_t(I) * 4 + 255) / 256 * 256;  // fp32 hidden rows (bf16 paths use half)
-  const uint64_t mx = mx_workspace_layout(T, k, H, I).total, fp8 = fp8_ffn_workspace_bytes(T, k, H, I);
-  return size_t(std::max(b, std::max(mx, fp8)));
+  const uint64_t mx = mx_workspace_layout(T, k, H, I).total;
+  return size_t(b > mx ? b : mx);
 }
 
 // Block-wide: index of the aidx-th expert with a non-empty segment (ascending
@@ -786,7 +786,7 @@ static ft_status ffn_check(const ft_expert_layout *L, const void *slot_pool, int
   FT_REQUIRE(aligned(x, 16) && aligned(y_rows, 16) && (!y_shared || aligned(y_shared, 16)) &&
                  aligned(workspace, 16),
              "ft_moe_grouped_ffn: x, y_rows, y_shared, workspace must be 16-byte aligned");
-  const size_t need = ffn_workspace_bytes(T, k, E, H, I);
+  const size_t need = ffn_workspace_bytes(wd, T, k, H, I);
   FT_REQUIRE(workspace != nullptr && workspace_bytes >= need,
              "ft_moe_grouped_ffn: workspace too small (see ft_workspace_bytes)");
   return FT_OK;
@@ -1304,7 +1304,7 @@ extern "C" ft_status ft_moe_grouped_ffn_noalloc(const ft_expert_layout *L, const
   FT_REQUIRE(T >= 0 && k >= 1 && E >= 1 && L->H >= 1 && L->I >= 1,
              "ft_moe_grouped_ffn_noalloc: need T >= 0, k >= 1, E >= 1 and an initialised layout");
   FT_REQUIRE(int64_t(T) * (k + 1) < (int64_t(1) << 31), "ft_moe_grouped_ffn_noalloc: T*k too large");
-  const size_t need = ffn_workspace_bytes(T, k, E, L->H, L->I);
+  const size_t need = ffn_workspace_bytes(L->wdtype, T, k, L->H, L->I);
   if (need > kNoAllocScratchBytes)
     return fail(FT_ECAPACITY, "ft_moe_grouped_ffn_noalloc: this call needs " + std::to_string(need) +
                                   " bytes of scratch, above the static " + std::to_string(kNoAllocScratchBytes) +

@@ -114,8 +114,8 @@ extern "C" ft_status ft_fp8_quantize(const void *x, int32_t x_dtype, int64_t ldx
   FT_REQUIRE(n >= 0 && K >= 0, "ft_fp8_quantize: need n >= 0, K >= 0");
   FT_SUPPORTED(K % 16 == 0, "ft_fp8_quantize: K must be a multiple of 16");
   FT_REQUIRE(ldx >= K && ldc >= K, "ft_fp8_quantize: row pitch below K");
-  FT_SUPPORTED(n < (int64_t(1) << 31) && n * cdiv(K, kFp8Block) < (int64_t(1) << 34),
-               "ft_fp8_quantize: more than 2^31 rows or 2^34 blocks");
+  FT_SUPPORTED(n < (int64_t(1) << 31) && n * cdiv(K, kFp8Block) < (int64_t(1) << 28) - 16,  // 2^32 threads of 8 elements
+               "ft_fp8_quantize: 2^31 rows, or rows of 2^28 - 16 blocks together, or more");
   if (n == 0 || K == 0) {
     clear_error();
     return FT_OK;

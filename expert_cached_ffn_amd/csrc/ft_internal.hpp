@@ -30,7 +30,7 @@ inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_
 
 // Workspace sizes (bytes) of the calls that take one.
 size_t permute_workspace_bytes(int32_t T, int32_t k, int32_t E);
-size_t ffn_workspace_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I);
+size_t ffn_workspace_bytes(int32_t wdtype, int32_t T, int32_t k, int32_t H, int32_t I);
 
 // Validates the routing arguments of ft_moe_route and (launch) enqueues the
 // router logits when w_router != NULL; nothing else.

@@ -27,9 +27,10 @@ static ft_status launch_tiles(GroupArgs a, hipStream_t stream) {
   using G = GroupTile<TY, EP, WM, WN, MT, NT, STAGES>;
   a.n_ntiles = cdiv(a.N, G::NCOL);
   const int64_t items = int64_t(row_tiles(a, G::BM)) * a.n_ntiles;
-  FT_SUPPORTED(items < (int64_t(1) << 31) - 8, "grouped product: more than 2^31 tiles");
-  const unsigned grid = unsigned(cdiv<int64_t>(items, 8) * 8);
-  hipLaunchKernelGGL((group_gemm_kernel<TY, EP, WM, WN, MT, NT, STAGES>), dim3(grid), dim3(G::THREADS), 0, stream, a);
+  const int64_t grid = cdiv<int64_t>(items, 8) * 8;
+  FT_SUPPORTED(grid * G::THREADS < (int64_t(1) << 32), "grouped product: more tiles than a launch has workgroups");
+  hipLaunchKernelGGL((group_gemm_kernel<TY, EP, WM, WN, MT, NT, STAGES>), dim3(unsigned(grid)), dim3(G::THREADS), 0,
+                     stream, a);
   FT_LAUNCHED("group_gemm_kernel");
   return FT_OK;
 }

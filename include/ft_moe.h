@@ -227,9 +227,9 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  *   weights keep fp32 rows there.
  * workspace: ft_workspace_bytes(FT_WS_FFN, T, k, E, H, I) bytes.
  * Limits: FT_BF16 weights need H, I multiples of 128; FT_MXFP4 multiples of
- *   256; FT_FP8 multiples of 16; E <= 4096.  MXFP4 scale bytes must lie in 2..252 (every decoded value
- *   is then an exact bf16).  Buffers 16-byte aligned, slot_pool and blobs
- *   256-byte aligned.
+ *   256; FT_FP8 multiples of 16; E <= 4096.  MXFP4 scale bytes must lie in
+ *   2..252 (every decoded value is then an exact bf16).  Buffers 16-byte
+ *   aligned, slot_pool and blobs 256-byte aligned.
  */
 enum { FT_FFN_EXACT = 0, FT_FFN_NATIVE_MX = 1 };
 enum { FT_FFN_GATE_UP_ONLY = 0x100, FT_FFN_DOWN_ONLY = 0x200 };
@@ -248,7 +248,8 @@ ft_status ft_moe_grouped_ffn(const ft_expert_layout *L, const void *slot_pool, i
  * ft_noalloc_scratch_bytes() bytes (16 MiB) that each GPU the library runs on
  * holds until the process ends; its address on a GPU is resolved on the first
  * call there.  The call allocates nothing.
- * A call whose ft_workspace_bytes(FT_WS_FFN, T, k, E, H, I) exceeds that size
+ * A call that needs more (FT_FP8: ft_workspace_bytes(FT_WS_FFN, T, k, E, H, I);
+ * the other weights: without FT_FP8's part of it, up to a fifth less)
  * returns FT_ECAPACITY and enqueues nothing (decode batches fit: e.g. 64
  * tokens of H=2048, I=768, top-8, or 32 tokens of H=4096, I=2048, top-6 with a
  * shared expert, in either mode).
@@ -371,8 +372,9 @@ ft_status ft_mxfp8_quantize(const void *x, int64_t ldx, int32_t n, int32_t K, ui
  * ceil(K / 128)] fp32, row-major.  A block that holds a NaN or an infinity gets
  * scale NaN and codes 0, so every product over it is NaN; other blocks are not
  * touched by it.  Bytes of codes behind column K of a row are left as they were.
- * n = 0 or K = 0 is a no-op.  Errors: K not a multiple of 16, n >= 2^31 or more
- * than 2^34 blocks -> FT_ENOTSUP; x, codes not 16-byte aligned, ldx not a
+ * n = 0 or K = 0 is a no-op.  Errors: K not a multiple of 16, n >= 2^31, n rows
+ * of ceil(K / 128) blocks that make 2^28 - 16 or more (quantize slices of the
+ * rows) -> FT_ENOTSUP; x, codes not 16-byte aligned, ldx not a
  * multiple of 8, ldc of 16, a pitch below K, block_rows other than 1 and 128,
  * NULL pointers -> FT_EINVAL.
  */
@@ -787,7 +789,8 @@ enum { FT_WS_PERMUTE = 1, FT_WS_FFN = 2, FT_WS_ROUTE_PERMUTE = 3, FT_WS_LAYER = 
 
 /* Bytes of workspace the call `which` needs for these sizes (0 if none).
  * For FT_WS_FFN, H and I are those of the layout and the shared expert is
- * assumed present (an upper bound either way). */
+ * assumed present (an upper bound either way), for any weight type: FT_FP8
+ * needs the most. */
 size_t ft_workspace_bytes(int32_t which, int32_t T, int32_t k, int32_t E, int32_t H, int32_t I);
 
 #ifdef __cplusplus

@@ -58,6 +58,25 @@ def test_quantize_refusals():
     f(None, F32, 0, 5, 0, 128, None, 0, None, stream=0)        # K = 0
 
 
+def test_launch_limits():
+    # one launch holds 2^32 threads: 2^28 blocks of a quantizer's rows, 2^23 of the largest tiles
+    assert _err(ops.ft_fp8_quantize, 16, BF16, 128, (1 << 28) - 16, 128, 1, 16, 128, 16) == ENOTSUP
+    assert _err(ops.ft_fp8_quantize, 16, BF16, 1 << 24, 1 << 15, 1 << 24, 1, 16, 1 << 24, 16) == ENOTSUP
+    assert _err(ops.ft_fp8_gemm, 16, 16, 16, 16, 16, 16, (1 << 31) - 513, 4096, 16, BF16, 16, 4096) == ENOTSUP
+
+
+def test_workspace_of_other_weights_unchanged():
+    """FP8's FFN needs more than the others': their calls are not held to it.  (x is misaligned: nothing is launched.)"""
+    T, k, E, H, I = 600, 8, 128, 2048, 768
+    rows = T * (k + 1)
+    assert rows * I * 4 <= ops.ft_noalloc_scratch_bytes() < rows * I * 5
+    f = ops.ft_moe_grouped_ffn_noalloc
+    for wdtype, scratch in ((1, True), (FP8, False)):
+        L = ops.ft_expert_layout_init(wdtype, H, I)
+        got = _err(f, L, 256, None, None, 8, BF16, T, k, E, 256, 256, 256, None, 0, n_slots=E)
+        assert (got != -3) == scratch
+
+
 def test_gemm_refusals():
     f = ops.ft_fp8_gemm
     ok = dict(a=16, lda=256, a_scales=16, w=16, ldw=256, w_scales=16, M=4, N=8, K=256, out_dtype=BF16, out=16, ldo=8)
