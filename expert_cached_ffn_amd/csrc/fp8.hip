@@ -15,7 +15,9 @@
 //
 // The kernels only move bytes: 2 (or 4) in and 1 out per element.  A 16-lane row
 // of a wave holds one 1 x 128 block, 8 elements (16 bytes of bf16) per lane,
-// and takes the block's maximum with four DPP lane moves.
+// and takes the block's maximum with four DPP lane moves.  8192 x 4096 bf16 by
+// 1 x 128: 20.4 us, 5.0 TB/s read and written together (a device copy: 5.2);
+// a 4096 x 2048 weight by 128 x 128: 7.0 us, of which the launch is about 5.
 #include "ft_internal.hpp"
 #include "fp8_util.hpp"
 

@@ -20,6 +20,10 @@
 // the rule of fp8.hip (a lane's 32 elements and three other lanes' are one
 // block): one launch less, and the hidden vector of the FP8 experts keeps its
 // fp32 value until then.
+//
+// Measured: one row by 4096 x 4096 FP8 7.3 us, 77 rows by 1001 x 2000 in fp32
+// 7.2 us, one launch being about 5 of both; the FP8 experts' down product of 33
+// tokens (H 2048, I 768, about 104 experts' weights, 164 MB) 47 us.
 #pragma once
 
 #include "group_gemm.hpp"
