@@ -224,7 +224,8 @@ ft_status ft_moe_route_permute(const void *x, int32_t x_dtype, const void *w_rou
  *   stages.  Both bits: FT_EINVAL.  For bf16 and MXFP4 weights the hidden
  *   rows are bf16 [T*k (+T), I] at the start of the workspace: row p of the
  *   permuted order, then the shared expert's row of token t at T*k + t; fp32
- *   weights keep fp32 rows there.
+ *   weights keep fp32 rows there; the form of FT_FP8's rows is not fixed (they
+ *   come from a FT_FFN_GATE_UP_ONLY call of the same T, k, E and layout).
  * workspace: ft_workspace_bytes(FT_WS_FFN, T, k, E, H, I) bytes.
  * Limits: FT_BF16 weights need H, I multiples of 128; FT_MXFP4 multiples of
  *   256; FT_FP8 multiples of 16; E <= 4096.  MXFP4 scale bytes must lie in
@@ -398,7 +399,8 @@ ft_status ft_fp8_quantize(const void *x, int32_t x_dtype, int64_t ldx, int64_t n
  * 2e-4 of the block's sum of magnitudes), the blocks being added in fp32.
  * Codes 0x7f / 0xff are NaN.  M = 0 or N = 0 is a no-op.
  * Limits (FT_ENOTSUP): K a multiple of 16, pitches of a and w at most 4 MiB,
- * M < 2^31 - 512.  FT_EINVAL: a, w or out not 16-byte aligned, lda or ldw not
+ * M < 2^31 - 512, out of fewer than about 2^39 elements (2^23 tiles of 256 x
+ * 256).  FT_EINVAL: a, w or out not 16-byte aligned, lda or ldw not
  * a multiple of 16 or below K, ldo below N, K < 1, NULL pointers.
  */
 ft_status ft_fp8_gemm(const uint8_t *a, int64_t lda, const float *a_scales, const uint8_t *w, int64_t ldw,
